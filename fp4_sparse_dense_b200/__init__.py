@@ -7,7 +7,10 @@ buffers with torch. There is no CPU fallback: if the library is missing or the d
 not an sm_100 GPU the calls raise.
 
 Low-level names mirror the C entry points (``sharq_prepare``, ``sharq_linear`` ...);
-``quantize_weight``, ``prepare`` and ``linear`` are the tensor-level conveniences.
+``quantize_weight``, ``prepare`` and ``linear`` are the tensor-level conveniences; the
+few-row product with 16-bit activations (``matvec``) and the experts' operators
+(``sort_tokens``, ``expert_matvec``, ``combine_tokens`` and their gradients) are in
+``experts.py`` and exported from here.
 """
 from __future__ import annotations
 
@@ -23,7 +26,9 @@ from ._abi import (  # noqa: F401
     sharq_read_device_status,
     sharq_prepare, sharq_quantize_weight, sharq_linear, sharq_linear_workspace_size,
     sharq_linear_noalloc, sharq_prepare_rmsnorm, sharq_wait_probe, sharq_prepare_alongside,
-    sharq_prepare_given_amax,
+    sharq_prepare_given_amax, sharq_matvec, sharq_sort_tokens, sharq_sort_tokens_backward,
+    sharq_expert_matvec, sharq_combine_tokens, sharq_combine_tokens_backward, sharq_tokens,
+    sharq_expert_weights,
 )
 
 __all__ = [
@@ -34,6 +39,10 @@ __all__ = [
     "sharq_read_device_status",
     "sharq_status_string", "SharqError", "linear_workspace",
     "NVFP4", "MXFP4", "PAIR_4_8", "ELEM_2_4", "F16", "BF16", "F32",
+    "matvec", "ExpertWeights", "quantize_experts", "SortedTokens", "sort_tokens",
+    "sort_tokens_backward", "expert_matvec", "combine_tokens", "combine_tokens_backward",
+    "sharq_matvec", "sharq_sort_tokens", "sharq_sort_tokens_backward", "sharq_expert_matvec",
+    "sharq_combine_tokens", "sharq_combine_tokens_backward",
 ]
 
 
@@ -254,3 +263,9 @@ def linear(act: PreparedAct, w: QuantWeight, out=None, out_dtype=None, workspace
     check(sharq_linear(ctypes.byref(ca), ctypes.byref(cw), _ptr(out), code, ws_ptr, ws_bytes,
                        _stream(stream, out.device)))
     return out
+
+
+from .experts import (  # noqa: E402,F401
+    ExpertWeights, SortedTokens, combine_tokens, combine_tokens_backward, expert_matvec, matvec,
+    quantize_experts, sort_tokens, sort_tokens_backward,
+)

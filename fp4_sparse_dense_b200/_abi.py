@@ -47,6 +47,19 @@ class sharq_weight_bytes(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in ("codes", "scales_dense", "scales_sparse")]
 
 
+class sharq_tokens(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("order", ctypes.c_void_p),
+                ("place", ctypes.c_void_p), ("T", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("E", ctypes.c_int32)]
+
+
+class sharq_expert_weights(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales_dense", ctypes.c_void_p),
+                ("scales_sparse", ctypes.c_void_p), ("tensor_scale", ctypes.c_void_p),
+                ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("cfg", sharq_config)]
+
+
 def _load():
     if not os.path.exists(lib_path):
         raise ImportError(
@@ -54,6 +67,8 @@ def _load():
             "`python -m fp4_sparse_dense_b200.build`. There is no CPU fallback.")
     L = ctypes.CDLL(lib_path)
     vp, st = ctypes.c_void_p, ctypes.c_int
+    i32, sz = ctypes.c_int32, ctypes.c_size_t
+    tok, ew = ctypes.POINTER(sharq_tokens), ctypes.POINTER(sharq_expert_weights)
     sig = {
         "sharq_act_sizes": (st, [ctypes.c_int32, ctypes.c_int32, sharq_config,
                                  ctypes.POINTER(sharq_act_bytes)]),
@@ -71,6 +86,12 @@ def _load():
                                              sharq_config, ctypes.POINTER(ctypes.c_size_t)]),
         "sharq_linear_noalloc": (st, [ctypes.POINTER(sharq_act), ctypes.POINTER(sharq_weight),
                                       vp, ctypes.c_int, vp]),
+        "sharq_matvec": (st, [vp, sz, i32, st, ctypes.POINTER(sharq_weight), vp, sz, st, vp]),
+        "sharq_sort_tokens": (st, [vp, i32, tok, vp, sz, i32, st, vp, sz, vp]),
+        "sharq_sort_tokens_backward": (st, [vp, sz, i32, st, tok, vp, sz, vp]),
+        "sharq_expert_matvec": (st, [vp, sz, i32, st, tok, ew, vp, sz, st, vp]),
+        "sharq_combine_tokens": (st, [vp, sz, i32, st, tok, vp, vp, sz, vp]),
+        "sharq_combine_tokens_backward": (st, [vp, sz, vp, sz, i32, st, tok, vp, vp, sz, vp, vp]),
         "sharq_device_status": (st, []),
         "sharq_read_device_status": (st, [vp]),
         "sharq_wait_probe": (st, [vp, ctypes.c_uint32, ctypes.c_uint64, vp]),
@@ -94,6 +115,12 @@ sharq_prepare_rmsnorm = lib.sharq_prepare_rmsnorm
 sharq_linear = lib.sharq_linear
 sharq_linear_workspace_size = lib.sharq_linear_workspace_size
 sharq_linear_noalloc = lib.sharq_linear_noalloc
+sharq_matvec = lib.sharq_matvec
+sharq_sort_tokens = lib.sharq_sort_tokens
+sharq_sort_tokens_backward = lib.sharq_sort_tokens_backward
+sharq_expert_matvec = lib.sharq_expert_matvec
+sharq_combine_tokens = lib.sharq_combine_tokens
+sharq_combine_tokens_backward = lib.sharq_combine_tokens_backward
 sharq_device_status = lib.sharq_device_status
 sharq_read_device_status = lib.sharq_read_device_status
 sharq_wait_probe = lib.sharq_wait_probe

@@ -1,0 +1,80 @@
+// Declarations shared by the translation units of the 16-bit-activation operators
+// (matvec.cu, tokens.cu) and the C ABI (sharq_api.cu). Not part of the ABI.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "sharq.h"
+
+namespace sharq {
+
+// Scale bytes of a weight as the few-row products read them: E4M3 per 16 or 32 elements of
+// K, or E8M0 per 32.
+enum ScaleView { kE4M3x16 = 0, kE4M3x32 = 1, kE8M0x32 = 2 };
+
+struct MatvecParams {
+  const void* X;          // [rows][K] 16-bit, row pitch ldx elements
+  const uint8_t* codes;   // [N][K/2]
+  const uint8_t* scales;  // tiled, N x K/16 or N x K/32
+  const float* w_scale;   // tensor scale (device)
+  void* Y;                // [rows][N], row pitch ldy elements
+  size_t ldx, ldy;
+  int M, N, K;
+  int y_dtype;            // sharq_dtype
+  // experts: E weights one after another, rows sorted by expert (E == 0: one weight, M rows)
+  const int32_t* offsets;  // [E + 1] first row of each expert
+  const int32_t* order;    // row p belongs to assignment order[p], i.e. token order[p] / k,
+                           // and X holds tokens; null: X holds the sorted rows themselves
+  int E, k;
+  size_t codes_stride, scales_stride;  // bytes from one expert's weight to the next
+};
+
+cudaError_t launch_matvec(const MatvecParams& p, bool bf16, ScaleView view, cudaStream_t st);
+
+struct SortParams {
+  const void* experts;  // [T * k] int32 or int64
+  int ids64;
+  int n, k, E;
+  int32_t* offsets;
+  int32_t* order;
+  int32_t* place;
+};
+cudaError_t launch_sort(const SortParams& p, cudaStream_t st);
+
+// Rows moved between token order and expert order. H elements of `dtype` per row; every
+// matrix has a row pitch in elements.
+struct RowsParams {
+  const int32_t* place;  // [T * k] sorted row of each assignment, < 0: dropped
+  const float* weights;  // [T * k] or null (1)
+  const void* tokens_in; // [T][H]
+  const void* rows_in;   // [n][H]
+  void* tokens_out;
+  void* rows_out;
+  float* d_weights;      // [T * k]
+  size_t ld_tokens_in, ld_rows_in, ld_tokens_out, ld_rows_out;
+  int T, k, H;
+};
+enum RowsOp { kGather = 0, kCombine = 1, kCombineGrad = 2 };
+cudaError_t launch_rows(const RowsParams& p, RowsOp op, int dtype, cudaStream_t st);
+
+// Launches `kern` with the programmatic-stream-serialization attribute: it may start while
+// the kernel before it on the stream finishes, and waits (griddepcontrol.wait) before it
+// touches anything that kernel reads or writes.
+template <typename... Args>
+inline cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, unsigned threads,
+                                    size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace sharq

@@ -9,6 +9,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "experts_internal.h"
 #include "sharq_internal.h"
 
 namespace sharq {
@@ -416,6 +417,83 @@ sharq_status prepare_impl(const void* X, sharq_dtype dtype, const sharq_act* a, 
 
 namespace sharq {
 namespace {
+
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+size_t element_bytes(sharq_dtype t) { return t == SHARQ_F32 ? 4 : 2; }
+
+bool is_dtype(sharq_dtype t) { return t == SHARQ_F16 || t == SHARQ_BF16 || t == SHARQ_F32; }
+
+// The weight part shared by sharq_matvec and sharq_expert_matvec: checks, the scale view and
+// the parameters of one weight.
+sharq_status matvec_weight(const void* X, size_t ldx, sharq_dtype dtype, void* codes,
+                           void* scales_dense, void* scales_sparse, const float* tensor_scale,
+                           int32_t K, int32_t N, sharq_config cfg, void* Y, size_t ldy,
+                           sharq_dtype y_dtype, MatvecParams* p, ScaleView* view) {
+  sharq_weight_bytes sz;
+  sharq_status s = weight_sizes(K, N, cfg, &sz);
+  if (s != SHARQ_OK) return s;
+  if ((dtype != SHARQ_F16 && dtype != SHARQ_BF16) || !is_dtype(y_dtype)) return SHARQ_ERR_INVALID_ARG;
+  const bool pair = is_pair_mask(cfg.mask);
+  const void* scales = pair ? scales_sparse : scales_dense;
+  if (!codes || !scales || !tensor_scale) return SHARQ_ERR_INVALID_ARG;
+  if (ldx < size_t(K) || ldy < size_t(N)) return SHARQ_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(codes) || !aligned16(scales) || ldx % 8 != 0 ||
+      !aligned_to(tensor_scale, 4))
+    return SHARQ_ERR_MISALIGNED;
+  *view = cfg.fmt == SHARQ_MXFP4 ? kE8M0x32 : pair ? kE4M3x32 : kE4M3x16;
+  std::memset(p, 0, sizeof(*p));
+  p->X = X;
+  p->ldx = ldx;
+  p->codes = static_cast<const uint8_t*>(codes);
+  p->scales = static_cast<const uint8_t*>(scales);
+  p->w_scale = tensor_scale;
+  p->Y = Y;
+  p->ldy = ldy;
+  p->N = N;
+  p->K = K;
+  p->y_dtype = y_dtype;
+  p->k = 1;
+  p->codes_stride = sz.codes;
+  p->scales_stride = pair ? sz.scales_sparse : sz.scales_dense;
+  return SHARQ_OK;
+}
+
+sharq_status check_tokens(const sharq_tokens* t) {
+  if (!t || t->T < 0 || t->k < 1 || t->E < 1 || !t->offsets) return SHARQ_ERR_INVALID_ARG;
+  if (t->E > 1024 || size_t(t->T) * size_t(t->k) >= (size_t(1) << 30)) return SHARQ_ERR_UNSUPPORTED;
+  if (t->T > 0 && (!t->order || !t->place)) return SHARQ_ERR_INVALID_ARG;
+  if (!aligned_to(t->offsets, 4) || !aligned_to(t->order, 4) || !aligned_to(t->place, 4))
+    return SHARQ_ERR_MISALIGNED;
+  return SHARQ_OK;
+}
+
+// One [.][H] matrix of the row moves.
+sharq_status check_rows(const void* m, size_t ld, int32_t H, sharq_dtype dtype) {
+  if (!m || H < 1 || ld < size_t(H) || !is_dtype(dtype)) return SHARQ_ERR_INVALID_ARG;
+  return aligned_to(m, element_bytes(dtype)) ? SHARQ_OK : SHARQ_ERR_MISALIGNED;
+}
+
+RowsParams rows_params(const sharq_tokens* t, int32_t H) {
+  RowsParams r;
+  std::memset(&r, 0, sizeof(r));
+  r.place = t->place;
+  r.T = t->T;
+  r.k = t->k;
+  r.H = H;
+  return r;
+}
+
+sharq_status run_rows(const RowsParams& r, RowsOp op, sharq_dtype dtype, void* stream) {
+  DeviceInfo d;
+  sharq_status s = device_info(&d);
+  if (s != SHARQ_OK || r.T == 0) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  s = from_cuda(launch_rows(r, op, dtype, st));
+  note_launch(d, st, s == SHARQ_OK);
+  return s;
+}
+
 // One thread waits for *flag == expected with the same bounded-wait discipline as the
 // GEMM's pipeline waits; on expiry the status word gets SHARQ_ERR_TIMEOUT.
 __global__ void wait_probe_kernel(const uint32_t* flag, uint32_t expected, uint64_t limit_ns,
@@ -677,6 +755,137 @@ sharq_status sharq_linear(const sharq_act* a, const sharq_weight* w, void* Y, sh
   if (own) return from_cuda(launch_gemm_two(maps, p, y_dtype == SHARQ_F32, d.num_sms, st));
   return from_cuda(launch_gemm(maps, p, a->cfg.fmt, a->cfg.mask, res, y_dtype == SHARQ_F32,
                                d.num_sms, st));
+}
+
+sharq_status sharq_matvec(const void* X, size_t ldx, int32_t M, sharq_dtype dtype,
+                          const sharq_weight* w, void* Y, size_t ldy, sharq_dtype y_dtype,
+                          void* stream) {
+  if (!w || M < 0 || (M > 0 && (!X || !Y))) return SHARQ_ERR_INVALID_ARG;
+  MatvecParams p;
+  ScaleView view;
+  sharq_status s = matvec_weight(X, ldx, dtype, w->codes, w->scales_dense, w->scales_sparse,
+                                 w->tensor_scale, w->K, w->N, w->cfg, Y, ldy, y_dtype, &p, &view);
+  if (s != SHARQ_OK) return s;
+  if (M > (1 << 21)) return SHARQ_ERR_UNSUPPORTED;
+  p.M = M;
+  DeviceInfo d;
+  if ((s = device_info(&d)) != SHARQ_OK || M == 0) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  s = from_cuda(launch_matvec(p, dtype == SHARQ_BF16, view, st));
+  note_launch(d, st, s == SHARQ_OK);
+  return s;
+}
+
+sharq_status sharq_expert_matvec(const void* X, size_t ldx, int32_t gather, sharq_dtype dtype,
+                                 const sharq_tokens* t, const sharq_expert_weights* w, void* Y,
+                                 size_t ldy, sharq_dtype y_dtype, void* stream) {
+  sharq_status s = check_tokens(t);
+  if (s != SHARQ_OK) return s;
+  if (!w || w->E != t->E || (gather != 0 && gather != 1)) return SHARQ_ERR_INVALID_ARG;
+  if (t->T > 0 && (!X || !Y)) return SHARQ_ERR_INVALID_ARG;
+  MatvecParams p;
+  ScaleView view;
+  s = matvec_weight(X, ldx, dtype, w->codes, w->scales_dense, w->scales_sparse, w->tensor_scale,
+                    w->K, w->N, w->cfg, Y, ldy, y_dtype, &p, &view);
+  if (s != SHARQ_OK) return s;
+  p.M = t->T * t->k;
+  if (p.M > (1 << 19)) return SHARQ_ERR_UNSUPPORTED;
+  p.E = w->E;
+  p.k = t->k;
+  p.offsets = t->offsets;
+  p.order = gather ? t->order : nullptr;
+  DeviceInfo d;
+  if ((s = device_info(&d)) != SHARQ_OK || p.M == 0) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  s = from_cuda(launch_matvec(p, dtype == SHARQ_BF16, view, st));
+  note_launch(d, st, s == SHARQ_OK);
+  return s;
+}
+
+sharq_status sharq_sort_tokens(const void* experts, int32_t id_bits, const sharq_tokens* t,
+                               const void* X, size_t ldx, int32_t H, sharq_dtype dtype,
+                               void* rows, size_t ld_rows, void* stream) {
+  sharq_status s = check_tokens(t);
+  if (s != SHARQ_OK) return s;
+  if ((id_bits != 32 && id_bits != 64) || (t->T > 0 && !experts)) return SHARQ_ERR_INVALID_ARG;
+  if (!aligned_to(experts, size_t(id_bits) / 8)) return SHARQ_ERR_MISALIGNED;
+  RowsParams r = rows_params(t, H);
+  const bool move = X != nullptr && t->T > 0;
+  if (move) {
+    if ((s = check_rows(X, ldx, H, dtype)) != SHARQ_OK) return s;
+    if ((s = check_rows(rows, ld_rows, H, dtype)) != SHARQ_OK) return s;
+    r.tokens_in = X;
+    r.ld_tokens_in = ldx;
+    r.rows_out = rows;
+    r.ld_rows_out = ld_rows;
+  }
+  DeviceInfo d;
+  if ((s = device_info(&d)) != SHARQ_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  SortParams p;
+  p.experts = experts;
+  p.ids64 = id_bits == 64;
+  p.n = t->T * t->k;
+  p.k = t->k;
+  p.E = t->E;
+  p.offsets = t->offsets;
+  p.order = t->order;
+  p.place = t->place;
+  s = from_cuda(launch_sort(p, st));
+  note_launch(d, st, s == SHARQ_OK);
+  if (s != SHARQ_OK || !move) return s;
+  return from_cuda(launch_rows(r, kGather, dtype, st));
+}
+
+sharq_status sharq_sort_tokens_backward(const void* d_rows, size_t ld_d_rows, int32_t H,
+                                        sharq_dtype dtype, const sharq_tokens* t, void* dX,
+                                        size_t ld_dx, void* stream) {
+  return sharq_combine_tokens(d_rows, ld_d_rows, H, dtype, t, nullptr, dX, ld_dx, stream);
+}
+
+sharq_status sharq_combine_tokens(const void* rows, size_t ld_rows, int32_t H, sharq_dtype dtype,
+                                  const sharq_tokens* t, const float* weights, void* Y, size_t ldy,
+                                  void* stream) {
+  sharq_status s = check_tokens(t);
+  if (s != SHARQ_OK) return s;
+  RowsParams r = rows_params(t, H);
+  if (t->T > 0) {
+    if ((s = check_rows(rows, ld_rows, H, dtype)) != SHARQ_OK) return s;
+    if ((s = check_rows(Y, ldy, H, dtype)) != SHARQ_OK) return s;
+    if (!aligned_to(weights, 4)) return SHARQ_ERR_MISALIGNED;
+  }
+  r.rows_in = rows;
+  r.ld_rows_in = ld_rows;
+  r.tokens_out = Y;
+  r.ld_tokens_out = ldy;
+  r.weights = weights;
+  return run_rows(r, kCombine, dtype, stream);
+}
+
+sharq_status sharq_combine_tokens_backward(const void* dY, size_t ld_dy, const void* rows,
+                                           size_t ld_rows, int32_t H, sharq_dtype dtype,
+                                           const sharq_tokens* t, const float* weights,
+                                           void* d_rows, size_t ld_d_rows, float* d_weights,
+                                           void* stream) {
+  sharq_status s = check_tokens(t);
+  if (s != SHARQ_OK) return s;
+  RowsParams r = rows_params(t, H);
+  if (t->T > 0) {
+    if ((s = check_rows(dY, ld_dy, H, dtype)) != SHARQ_OK) return s;
+    if ((s = check_rows(rows, ld_rows, H, dtype)) != SHARQ_OK) return s;
+    if ((s = check_rows(d_rows, ld_d_rows, H, dtype)) != SHARQ_OK) return s;
+    if (!weights || !d_weights) return SHARQ_ERR_INVALID_ARG;
+    if (!aligned_to(weights, 4) || !aligned_to(d_weights, 4)) return SHARQ_ERR_MISALIGNED;
+  }
+  r.tokens_in = dY;
+  r.ld_tokens_in = ld_dy;
+  r.rows_in = rows;
+  r.ld_rows_in = ld_rows;
+  r.rows_out = d_rows;
+  r.ld_rows_out = ld_d_rows;
+  r.weights = weights;
+  r.d_weights = d_weights;
+  return run_rows(r, kCombineGrad, dtype, stream);
 }
 
 sharq_status sharq_wait_probe(const uint32_t* flag, uint32_t expected, uint64_t limit_ns,

@@ -261,6 +261,94 @@ SHARQ_API sharq_status sharq_linear_workspace_size(int32_t M, int32_t N, int32_t
 SHARQ_API sharq_status sharq_linear_noalloc(const sharq_act* act, const sharq_weight* w, void* Y,
                                             sharq_dtype y_dtype, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Few-row products with 16-bit activations, and experts
+ *
+ * These calls (no counterpart in the SharQ page) use the weight payload above without
+ * preparing the activations: a decoded token's row goes into the product as it is. Their
+ * matrices have a row pitch in elements (ld >= the row's length), so a view of a larger
+ * matrix can be passed. T = 0 or no rows at all is allowed and writes nothing but offsets. */
+
+/* Y[M x N] = s_gw * X[M x K] * deq(W): the activations stay in 16 bits. Products are exact
+ * (E2M1 * scale has at most 6 significant bits), sums are float32 in a fixed order, and Y is
+ * rounded once. X: device [M][K], `dtype` F16 or BF16, 16-byte aligned, ldx % 8 == 0. w: any
+ * configuration; pair masks are read through scales_sparse, the others through scales_dense.
+ * Y: device [M][N], F16, BF16 or F32. Infinite and NaN activations reach the outputs of
+ * their own row as in a float32 product. The weight is read once per 32 rows: for many rows
+ * sharq_prepare + sharq_linear is the faster path. M <= 2^21 (else SHARQ_ERR_UNSUPPORTED). */
+SHARQ_API sharq_status sharq_matvec(const void* X, size_t ldx, int32_t M, sharq_dtype dtype,
+                                    const sharq_weight* w, void* Y, size_t ldy,
+                                    sharq_dtype y_dtype, void* stream);
+
+/* The order of T tokens by expert, k assignments each (assignment a = t * k + j). Caller-owned
+ * device buffers, filled by sharq_sort_tokens:
+ *   offsets [E + 1]  first sorted row of each expert; offsets[E]: number of kept assignments
+ *   order   [T * k]  assignment of each sorted row; dropped assignments follow the kept ones
+ *   place   [T * k]  sorted row of each assignment, -1 for a dropped one
+ * 1 <= E <= 1024, k >= 1, T * k < 2^30. The calls below trust these contents. */
+typedef struct {
+  int32_t* offsets;
+  int32_t* order;
+  int32_t* place;
+  int32_t T, k, E;
+} sharq_tokens;
+
+/* E quantised weights of one shape and configuration, one after another in each buffer (every
+ * expert's part as sharq_weight_sizes gives it; tensor_scale: 4 floats per expert). Expert e
+ * is a sharq_weight at these offsets, to be filled by sharq_quantize_weight. */
+typedef struct {
+  void* codes;
+  void* scales_dense;
+  void* scales_sparse;
+  float* tensor_scale;
+  int32_t K, N, E;
+  sharq_config cfg;
+} sharq_expert_weights;
+
+/* Sorts the assignments by expert (stable: equal experts keep the order of a) and, where X is
+ * not null, gathers rows[p] = X[order[p] / k] for p < offsets[E]; rows behind that are left
+ * as they were. experts: device [T][k] int32 (id_bits 32) or int64 (64); an id outside
+ * [0, E) is dropped. X: device [T][H], rows: device [T * k][H], any H >= 1, dtype F16, BF16
+ * or F32, aligned to their elements (16-byte rows are fastest). */
+SHARQ_API sharq_status sharq_sort_tokens(const void* experts, int32_t id_bits,
+                                         const sharq_tokens* tokens, const void* X, size_t ldx,
+                                         int32_t H, sharq_dtype dtype, void* rows,
+                                         size_t ld_rows, void* stream);
+
+/* Gradient of the gather: dX[t] = sum over t's kept assignments of d_rows[place]. Summed in
+ * float32 in increasing j, rounded once; 0 for a token without any. Arguments as above. */
+SHARQ_API sharq_status sharq_sort_tokens_backward(const void* d_rows, size_t ld_d_rows, int32_t H,
+                                                  sharq_dtype dtype, const sharq_tokens* tokens,
+                                                  void* dX, size_t ld_dx, void* stream);
+
+/* Y[p] = X row of sorted row p * deq(W of its expert), as sharq_matvec, for p < offsets[E];
+ * rows behind that are left as they were. gather == 0: X holds the sorted rows [T * k][K];
+ * gather == 1: X holds the tokens [T][K] and row p reads token order[p] / k. tokens->E must
+ * equal w->E. */
+SHARQ_API sharq_status sharq_expert_matvec(const void* X, size_t ldx, int32_t gather,
+                                           sharq_dtype dtype, const sharq_tokens* tokens,
+                                           const sharq_expert_weights* w, void* Y, size_t ldy,
+                                           sharq_dtype y_dtype, void* stream);
+
+/* Y[t] = sum over t's kept assignments of weights[t][j] * rows[place], in float32 in
+ * increasing j, rounded once; 0 for a token without any. weights: device float [T][k], or
+ * null for 1. Rows and weights of dropped assignments are not read. */
+SHARQ_API sharq_status sharq_combine_tokens(const void* rows, size_t ld_rows, int32_t H,
+                                            sharq_dtype dtype, const sharq_tokens* tokens,
+                                            const float* weights, void* Y, size_t ldy,
+                                            void* stream);
+
+/* Gradients of the combination: d_rows[place] = weights[t][j] * dY[t] (rows behind the last
+ * sorted one are left as they were) and d_weights[t][j] = <dY[t], rows[place]> in float32, 0
+ * for a dropped assignment. d_rows may be rows itself. */
+SHARQ_API sharq_status sharq_combine_tokens_backward(const void* dY, size_t ld_dy,
+                                                     const void* rows, size_t ld_rows, int32_t H,
+                                                     sharq_dtype dtype,
+                                                     const sharq_tokens* tokens,
+                                                     const float* weights, void* d_rows,
+                                                     size_t ld_d_rows, float* d_weights,
+                                                     void* stream);
+
 /* Failure-detection self-test (no counterpart in the pages): launches one thread that
  * waits until the device word *flag equals `expected`, for at most limit_ns nanoseconds
  * (1 ms ... 10 s). On expiry it records SHARQ_ERR_TIMEOUT in the status word of `stream`
