@@ -27,10 +27,15 @@ struct MatvecParams {
   const int32_t* order;    // row p belongs to assignment order[p], i.e. token order[p] / k,
                            // and X holds tokens; null: X holds the sorted rows themselves
   int E, k;
+  int early;  // the weight may be loaded before the kernel launched just before has completed
+  int splits;  // CTAs of a cluster along K (set by launch_matvec)
+  int x_rows;     // rows of activations that stay in shared memory (set by launch_matvec)
+  int out_units;  // units whose sums a CTA of a cluster holds (set by launch_matvec)
   size_t codes_stride, scales_stride;  // bytes from one expert's weight to the next
 };
 
-cudaError_t launch_matvec(const MatvecParams& p, bool bf16, ScaleView view, cudaStream_t st);
+cudaError_t launch_matvec(const MatvecParams& p, bool bf16, ScaleView view, int num_sms,
+                          cudaStream_t st);
 
 struct SortParams {
   const void* experts;  // [T * k] int32 or int64

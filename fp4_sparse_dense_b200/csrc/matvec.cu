@@ -5,17 +5,37 @@
 //
 // The weight is read once, as it lies: K/2 code bytes and K/B scale bytes per output n,
 // which bounds the call (0.53 or 0.56 bytes per weight element against 2 M flops). A warp
-// owns 32 outputs and a share of K. In a step of 128 K each of its lanes loads 16 code bytes
-// (32 consecutive K) of four outputs, widens them in registers and feeds mma.sync
-// (m16n8k16, float32 accumulators) with the codes as the A operand and eight activation
-// rows as B: with so few rows the tensor pipe has time to spare, and operands that go from
-// the load straight into registers need neither shared memory nor tensor memory on the way.
-// K's order inside a step is free as long as both operands share it, so the lane's own 32 K
-// are its k indices in all eight MMAs of the step and no code moves between lanes.
+// takes 32 outputs and steps of 128 K. In a step each lane holds 16 code bytes (32
+// consecutive K) of four outputs, widens them in registers and feeds mma.sync (m16n8k16,
+// float32 accumulators) with the weight as the A operand and eight activation rows as B. With
+// so few rows the tensor pipe has time to spare, and the widened operands go from registers
+// into the MMA without a way back through shared or tensor memory. K's order inside a step is
+// free as long as both operands share it, so the lane's own 32 K are its k indices in all
+// eight MMAs of the step and no code moves between lanes. The weight streams through rings of
+// asynchronous copies; the sums of the warps and CTAs that share an output meet in shared
+// memory, in a fixed order.
 //
-// Rounding: e2m1 * sf has at most 6 significant bits (E8M0: 2), exact in bf16; bf16
-// activations enter as they are and fp16 ones as the exact sum of two bf16 (8 + 3 bits), so
-// all products are exact and only the float32 sums and the output round.
+// The grid is one CTA per SM. A CTA keeps the activations of its slot (up to 8 MT rows of one
+// weight) in shared memory, read and converted once, and takes an equal run of the list of
+// 32-output units; its warps split the run's steps evenly, whatever unit they belong to, so
+// that there is one prologue and one sum per CTA and slot. Where the activations do not fit, a
+// cluster of S CTAs splits K and its CTAs add their sums through distributed shared memory.
+//
+// The widening sets the kernel's issue rate, so it uses the conversion instruction (two codes
+// to f16x2) and one packed multiply by the scale. That makes the weight an f16 operand:
+// - E4M3 scales: e2m1 * sf has at most 6 significant bits between 2^-10 and 2688: exact.
+// - E8M0 scales: relative to the row's first scale of the step, 2^(b - b_0), exact within
+//   2^-14 ... 2^13; the step's sum is multiplied by 2^(b_0 - 127) when it joins the
+//   accumulator. A wider spread takes passes over the step's codes, relative to the largest
+//   scale and 24 binades each.
+// - fp16 activations enter as they are. bf16 ones are scaled by a power of two per (row,
+//   step) so that the largest one's exponent is 15; exact for 32 binades, and the scale is
+//   taken out with the step's sum. Where some (row, step) of a CTA has a wider spread, or
+//   infinite or NaN values, the CTA's activations stay bf16 and the codes are widened to bf16
+//   by shifts and masks (about twice the instructions).
+// So every product is exact. The MMA's own additions cut bits below the accumulator's 24, so
+// an accumulator lives for one step (8 MMAs) and joins a float32 sum that rounds to nearest.
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -27,305 +47,809 @@
 namespace sharq {
 namespace {
 
-constexpr int kWarps = 8;       // warps of a CTA, which share the CTA's 32 outputs along K
-constexpr int kStepK = 128;     // K per warp step
-constexpr int kUnitRows = 32;   // outputs per CTA
+constexpr int kStepK = 128;   // K per warp step
+constexpr int kUnitRows = 32; // outputs per warp
 
-__device__ __forceinline__ uint4 load_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16_first(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
-__device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// Eight codes of a word -> four f16x2, codes (2 j, 2 j + 1) in word j.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t* h) {
+  asm volatile("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
 }
 
-// float value in both halves of a bf16x2 (exact for the values used here)
-__device__ __forceinline__ uint32_t both_bf16(float f) {
+// Two E4M3 bytes -> f16x2.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
   uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(d) : "f"(f));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(uint16_t(two)));
   return d;
 }
 
-// Multiplier of the widened codes (which carry a factor 2^-126) for one scale byte.
-// E4M3: sf * 2^118 (sf <= 448 keeps it finite; the products carry 2^-8 until the end). The
-// byte's seven bits in the float's exponent and mantissa are sf * 2^-120, subnormals
-// included.
-constexpr float kE4M3Tail = 256.f;  // takes the 2^-8 out again
-__device__ __forceinline__ uint32_t factor_e4m3(uint32_t c) {
-  const float v = __uint_as_float((c & 0x7Fu) << 20);
-  return both_bf16(__fmul_rn(__fmul_rn(v, 0x1p127f), 0x1p111f));
-}
-// E8M0: 2^(c - 127) itself, applied after the codes' 2^-126 has been taken out: no single
-// bf16 factor spans both.
-__device__ __forceinline__ uint32_t factor_e8m0(uint32_t c) {
-  return c ? c * 0x00800080u : 0x00400040u;
+// 2^d in both halves, for d in [-23, 0]; 0 outside.
+__device__ __forceinline__ uint32_t f16_pow2(int d) {
+  if (d > 0 || d < -23) return 0u;
+  const uint32_t h = d >= -14 ? uint32_t(d + 15) << 10 : 1u << (d + 24);
+  return h * 0x00010001u;
 }
 
-// Pair i of the word's eight codes: code i in the low half, code i + 4 in the high half, as
-// bf16 values times 2^-126 (the code's exponent and mantissa bits in bf16's, E2M1's subnormal
-// 0.5 as bf16's).
-template <int I>
-__device__ __forceinline__ uint32_t widen(uint32_t w) {
-  const uint32_t em = I == 0 ? w << 6 : I == 1 ? w << 2 : I == 2 ? w >> 2 : w >> 6;
-  const uint32_t sg = I == 0 ? w << 12 : I == 1 ? w << 8 : I == 2 ? w << 4 : w;
-  return (em & 0x01C001C0u) | (sg & 0x80008000u);
+__device__ __forceinline__ float pow2_normal(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
+
+// The same codes as bf16 values times 2^-126 (the code's exponent and mantissa bits in
+// bf16's, E2M1's subnormal 0.5 as bf16's): codes (i, i + 4) in word i. A masked nibble times
+// (2^6 + 2^12) has its value bits at 8..6 and its sign at 15.
+__device__ __forceinline__ void widen_bf16(uint32_t w, uint32_t* h) {
+  const uint32_t v = w >> 8;
+  h[0] = ((w & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
+  h[1] = ((w & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
+  h[2] = ((v & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
+  h[3] = ((v & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
+}
+
+// A warp's step of weight in shared memory: a lane's 16 code bytes of its four outputs, and
+// the scale words of the warp's 32 outputs (two 64-K chunks where there is a scale per 16 K).
+struct Stage {
+  uint4 codes[4][32];
+  uint4 scales[2][8];
+};
+
+// Eight bf16 activations of a (row, step) whose sixteen lanes call together -> f16, scaled by
+// a power of two; *undo takes it out again. *wide: their spread does not fit (infinite and
+// NaN values never do).
+__device__ __forceinline__ uint4 scale_bf16(uint4 v, float* undo, bool* wide) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  // largest magnitude, and 0xFFFF - (smallest non-zero one - 1), as 16-bit patterns
+  uint32_t top2 = 0, low2 = 0xFFFFFFFFu;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t m = w[j] & 0x7FFF7FFFu;
+    top2 = __vmaxu2(top2, m);
+    low2 = __vminu2(low2, __vsub2(m, 0x00010001u));
+  }
+  uint32_t key = __vmaxu2(__byte_perm(top2, ~low2, 0x5410), __byte_perm(top2, ~low2, 0x7632));
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) key = __vmaxu2(key, __shfl_xor_sync(0xFFFFFFFFu, key, d));
+  // subnormals count as the smallest normal exponent: their bits lie no deeper than its
+  const int top = max(int(key & 0xFFFFu) >> 7, 1);
+  const int low = max(int(0x10000u - (key >> 16)) >> 7, 1);  // no value but 0: 512
+  *wide = top - low >= 32 || top == 255;
+  const int shift = min(142 - top, 126);  // the largest exponent to 15
+  *undo = pow2_normal(-shift);
+  const uint32_t f = uint32_t(shift + 127) * 0x00800080u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t y = mul_bf16x2(w[j], f);
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+        : "=r"(w[j])
+        : "f"(__uint_as_float(y & 0xFFFF0000u)), "f"(__uint_as_float(y << 16)));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int VIEW>
-__device__ __forceinline__ uint32_t scaled(uint32_t w, uint32_t f) {
-  if (VIEW == kE8M0x32) w = mul_bf16x2(w, 0x7E807E80u);  // 2^126
-  return mul_bf16x2(w, f);
-}
+constexpr int kScaleStep = VIEW == kE4M3x16 ? 1024 : 512;  // scale bytes of 128 outputs x 128 K
 
-// Two activations (x[k], x[k + 4]) of the words X[k/2], X[k/2 + 2] for pair i.
-template <int I>
-__device__ __forceinline__ uint32_t pair_x(const uint4& v) {
-  const uint32_t a = I < 2 ? v.x : v.y, b = I < 2 ? v.z : v.w;
-  return __byte_perm(a, b, (I & 1) ? 0x7632 : 0x5410);
-}
-
-// fp16 pair -> the bf16 pair nearest to it and what that leaves, also bf16 (exact: 11 bits =
-// 8 + 3). Infinite and NaN values leave 0.
-__device__ __forceinline__ void split_f16(uint32_t h, uint32_t* hi, uint32_t* lo) {
-  const __half2 h2 = *reinterpret_cast<const __half2*>(&h);
-  const float2 f = __half22float2(h2);
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(f.y), "f"(f.x));
-  const float ax = __uint_as_float(d << 16), ay = __uint_as_float(d & 0xFFFF0000u);
-  const float rx = (h & 0x00007C00u) == 0x00007C00u ? 0.f : f.x - ax;
-  const float ry = (h & 0x7C000000u) == 0x7C000000u ? 0.f : f.y - ay;
-  uint32_t e;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(e) : "f"(ry), "f"(rx));
-  *hi = d;
-  *lo = e;
-}
-
-struct Stage {
-  uint4 c[4];  // codes of outputs r, r + 32, r + 64, r + 96
-  uint4 s;     // their scale words
+template <int MT>
+struct Acc {
+  float v[MT][2][4];  // (h, c): output 32 (2 h + c / 2) + g of the lane's quarter, row 2 t + c % 2
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[m][h][c] = 0.f;
+  }
 };
 
-template <int MT, bool BF16, int VIEW>
-__global__ void __launch_bounds__(kWarps * 32)
-matvec_kernel(const MatvecParams p) {
-  __shared__ float red[kWarps][kUnitRows][8 * MT + 1];
-  __shared__ int s_slot[3];  // expert, first row, rows
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
-
-  // which weight, and which of its rows
-  int e = 0, row0 = blockIdx.y * 8 * MT, rows = p.M - row0;
-  if (p.E > 0) {
-    if (warp == 0) {
-      // blockIdx.y counts chunks of 8 MT rows over all experts
-      int before = 0, found = -1, first = 0, count = 0;
-      for (int base = 0; base < p.E && found < 0; base += 32) {
-        const int ee = base + lane;
-        const int lo = ee < p.E ? p.offsets[ee] : 0, hi = ee < p.E ? p.offsets[ee + 1] : 0;
-        const int chunks = (hi - lo + 8 * MT - 1) / (8 * MT);
-        int incl = chunks;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-          if (lane >= d) incl += v;
-        }
-        const int start = before + incl - chunks;
-        const bool mine = int(blockIdx.y) >= start && int(blockIdx.y) < start + chunks;
-        const unsigned who = __ballot_sync(0xFFFFFFFFu, mine);
-        if (who) {
-          const int src = __ffs(who) - 1;
-          found = base + src;
-          const int c = int(blockIdx.y) - start;
-          first = __shfl_sync(0xFFFFFFFFu, lo + c * 8 * MT, src);
-          count = __shfl_sync(0xFFFFFFFFu, hi - lo - c * 8 * MT, src);
-        }
-        before += __shfl_sync(0xFFFFFFFFu, incl, 31);
-      }
-      if (lane == 0) {
-        s_slot[0] = found;
-        s_slot[1] = first;
-        s_slot[2] = count;
-      }
-    }
-    __syncthreads();
-    e = s_slot[0];
-    if (e < 0) return;
-    row0 = s_slot[1];
-    rows = s_slot[2];
-  }
-  rows = min(min(rows, 8 * MT), p.M - row0);
-
-  const int K = p.K, steps = K / kStepK;
-  const int nb = blockIdx.x >> 2, u = blockIdx.x & 3;  // 128-output group, quarter of its rows
-  const uint8_t* codes = p.codes + size_t(e) * p.codes_stride +
-                         size_t(nb * 128 + u * 8 + g) * (K / 2) + t * 16;
-  const size_t quarter = size_t(32) * (K / 2);
-  const uint8_t* scales;
-  if (VIEW == kE4M3x16)
-    scales = p.scales + size_t(e) * p.scales_stride +
-             (size_t(nb) * (K / 64) + (t >> 1)) * 512 + (u * 8 + g) * 16;
-  else
-    scales = p.scales + size_t(e) * p.scales_stride + size_t(nb) * steps * 512 + (u * 8 + g) * 16;
-  constexpr int kScaleStep = VIEW == kE4M3x16 ? 1024 : 512;
-
-  const uint16_t* x[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int r = m * 8 + g;
-    x[m] = nullptr;
-    if (r < rows) {
-      const int src = p.order && p.E > 0 ? p.order[row0 + r] / p.k : row0 + r;
-      x[m] = static_cast<const uint16_t*>(p.X) + size_t(src) * p.ldx + t * 32;
-    }
-  }
-
-  float acc[MT][2][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[m][h][c] = 0.f;
-
-  auto load = [&](int s, Stage& st) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) st.c[i] = load_stream(codes + i * quarter + size_t(s) * 64);
-    st.s = *reinterpret_cast<const uint4*>(scales + size_t(s) * kScaleStep);
-  };
-  auto compute = [&](int s, const Stage& st) {
-    const uint32_t sw[4] = {st.s.x, st.s.y, st.s.z, st.s.w};
-    uint32_t f[4][2];
+// One step with f16 operands. load_x(m, q): the lane's activations of row 8 m + g, K unit
+// 4 t + q of the step; load_undo(m): what takes the scaling of rows 8 m + 2 t and + 1 out.
+template <int MT, int VIEW, bool SCALED, typename LoadX, typename LoadUndo>
+__device__ __forceinline__ void step_f16(Acc<MT>& acc, const Stage& st, int rows, LoadX load_x,
+                                         LoadUndo load_undo) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const uint32_t pick = uint32_t(t) | uint32_t(4 + t) << 4;  // byte t of two words
+  const uint4 sv = st.scales[VIEW == kE4M3x16 ? t >> 1 : 0][g];
+  const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
+  int wp = 0, wpasses = 1;
+  bool narrow = true;
+  if (VIEW == kE8M0x32) {
+    uint32_t off = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (VIEW == kE4M3x16) {
-        const uint32_t two = sw[i] >> ((t & 1) * 16);
-        f[i][0] = factor_e4m3(two);
-        f[i][1] = factor_e4m3(two >> 8);
-      } else {
-        const uint32_t b = (sw[i] >> (t * 8)) & 0xFFu;
-        f[i][0] = f[i][1] = VIEW == kE8M0x32 ? factor_e8m0(b) : factor_e4m3(b);
+      const int d = int((sw[i] >> (8 * t)) & 0xFFu) - int(sw[i] & 0xFFu);
+      off |= uint32_t(d + 14) > 27u || ((sw[i] & 0xFFu) - 1u) > 189u;
+    }
+    narrow = __all_sync(0xFFFFFFFFu, off == 0);
+    if (!narrow) {
+      int spread = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b0 = sw[i] & 0xFFu, b1 = (sw[i] >> 8) & 0xFFu, b2 = (sw[i] >> 16) & 0xFFu,
+                  b3 = sw[i] >> 24;
+        spread = max(spread, max(max(b0, b1), max(b2, b3)) - min(min(b0, b1), min(b2, b3)));
+      }
+      wpasses = __reduce_max_sync(0xFFFFFFFFu, spread) / 24 + 1;
+    }
+  }
+  do {
+    uint32_t f[4][2];
+    float ref[4];  // power of two that the row's factors leave out
+    if (VIEW == kE4M3x16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t two = e4m3x2_f16x2(sw[i] >> ((t & 1) * 16));
+        f[i][0] = __byte_perm(two, two, 0x1010);
+        f[i][1] = __byte_perm(two, two, 0x3232);
+      }
+    } else if (VIEW == kE4M3x32) {
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const uint32_t two = e4m3x2_f16x2(__byte_perm(sw[i], sw[i + 1], pick));
+        f[i][0] = f[i][1] = __byte_perm(two, two, 0x1010);
+        f[i + 1][0] = f[i + 1][1] = __byte_perm(two, two, 0x3232);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = int((sw[i] >> (8 * t)) & 0xFFu);
+        int r;
+        if (narrow) {
+          r = int(sw[i] & 0xFFu);
+          f[i][0] = uint32_t(b - r + 15) * 0x04000400u;
+        } else {
+          const int b0 = sw[i] & 0xFFu, b1 = (sw[i] >> 8) & 0xFFu, b2 = (sw[i] >> 16) & 0xFFu,
+                    b3 = sw[i] >> 24;
+          const int top = max(max(b0, b1), max(b2, b3)) - 24 * wp;  // this pass: (top - 24, top]
+          r = max(top, 1);
+          f[i][0] = b <= top && b > top - 24 ? f16_pow2(b - r) : 0u;
+        }
+        ref[i] = __uint_as_float(uint32_t(r) << 23);
+        f[i][1] = f[i][0];
       }
     }
+    float part[MT][2][4];
+    const uint4 cw[4] = {st.codes[0][lane], st.codes[1][lane], st.codes[2][lane], st.codes[3][lane]};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint32_t a[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t w = q == 0 ? st.c[i].x : q == 1 ? st.c[i].y : q == 2 ? st.c[i].z : st.c[i].w;
-        const uint32_t ff = f[i][q >> 1];
-        a[i][0] = scaled<VIEW>(widen<0>(w), ff);
-        a[i][1] = scaled<VIEW>(widen<1>(w), ff);
-        a[i][2] = scaled<VIEW>(widen<2>(w), ff);
-        a[i][3] = scaled<VIEW>(widen<3>(w), ff);
+        const uint32_t w = q == 0 ? cw[i].x : q == 1 ? cw[i].y : q == 2 ? cw[i].z : cw[i].w;
+        widen(w, a[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[i][j] = mul_f16x2(a[i][j], f[i][q >> 1]);
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (MT > 1 && m * 8 >= rows) break;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (x[m]) v = *reinterpret_cast<const uint4*>(x[m] + size_t(s) * kStepK + q * 8);
-        uint32_t b[4] = {pair_x<0>(v), pair_x<1>(v), pair_x<2>(v), pair_x<3>(v)};
-        uint32_t lo[4];
-        if (!BF16) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) split_f16(b[i], &b[i], &lo[i]);
-        }
+        const uint4 b = load_x(m, q);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          mma_bf16(acc[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b[0], b[1]);
-          mma_bf16(acc[m][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b[2], b[3]);
-          if (!BF16) {
-            mma_bf16(acc[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], lo[0], lo[1]);
-            mma_bf16(acc[m][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], lo[2], lo[3]);
-          }
+          if (q == 0)
+            mma_f16_first(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
+          else
+            mma_f16(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
+          mma_f16(part[m][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
         }
       }
     }
-  };
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (MT > 1 && m * 8 >= rows) break;
+      float2 undo = make_float2(1.f, 1.f);
+      if (SCALED) undo = load_undo(m);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float v = part[m][h][c], x = c & 1 ? undo.y : undo.x;
+          float& to = acc.v[m][h][c];
+          if (VIEW == kE8M0x32)
+            to = fmaf(SCALED ? v * x : v, ref[2 * h + (c >> 1)], to);
+          else
+            to = SCALED ? fmaf(v, x, to) : to + v;
+        }
+    }
+  } while (VIEW == kE8M0x32 && ++wp < wpasses);
+}
 
-  Stage cur, nxt;
-  int s = warp;
-  if (s < steps) load(s, cur);
-  while (s < steps) {
-    const int n = s + kWarps;
-    if (n < steps) load(n, nxt);
-    compute(s, cur);
-    cur = nxt;
-    s = n;
+// One step with bf16 operands: the widened codes' 2^-126 is taken out by the scale's factor
+// (E4M3: sf * 2^118, finite up to 448; E8M0: 2^(126 + b - b_max)), the rest with the sum.
+// The codes go in step_f16's order, so that both kinds of operands give the same bits.
+template <int MT, int VIEW, typename LoadX>
+__device__ __forceinline__ void step_bf16(Acc<MT>& acc, const Stage& st, int rows, LoadX load_x) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const uint4 sv = st.scales[VIEW == kE4M3x16 ? t >> 1 : 0][g];
+  const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
+  uint32_t f[4][2];
+  float ref[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (VIEW == kE8M0x32) {
+      const int b0 = sw[i] & 0xFFu, b1 = (sw[i] >> 8) & 0xFFu, b2 = (sw[i] >> 16) & 0xFFu,
+                b3 = sw[i] >> 24;
+      const int top = max(max(max(b0, b1), max(b2, b3)), 1);
+      f[i][0] = f[i][1] =
+          uint32_t(max(int((sw[i] >> (8 * t)) & 0xFFu) - top + 253, 0)) * 0x00800080u;
+      ref[i] = __uint_as_float(uint32_t(top) << 23);
+    } else {
+#pragma unroll
+      for (int j = 0; j < (VIEW == kE4M3x16 ? 2 : 1); ++j) {
+        const uint32_t c = VIEW == kE4M3x16 ? sw[i] >> ((t & 1) * 16 + 8 * j) : sw[i] >> (t * 8);
+        // the byte's seven bits as a float's exponent and mantissa: sf * 2^-120
+        const float v = __uint_as_float((c & 0x7Fu) << 20) * 0x1p127f * 0x1p111f;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(f[i][j]) : "f"(v));
+      }
+      if (VIEW != kE4M3x16) f[i][1] = f[i][0];
+      ref[i] = 256.f;
+    }
   }
-
-  // accumulator (h, c) of a lane: output 16 h + 8 (c / 2) of its four, row 2 t + c % 2
+  float part[MT][2][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        red[warp][(2 * h + (c >> 1)) * 8 + g][m * 8 + 2 * t + (c & 1)] = acc[m][h][c];
-  __syncthreads();
-  const float scale = p.w_scale[size_t(e) * 4] * (VIEW == kE8M0x32 ? 1.f : kE4M3Tail);
-  for (int i = threadIdx.x; i < kUnitRows * rows; i += kWarps * 32) {
-    const int r = i & 31, m = i >> 5;
-    float v = 0.f;
+      for (int c = 0; c < 4; ++c) part[m][h][c] = 0.f;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    uint32_t a[4][4];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[w][r][m];
-    v *= scale;
-    const size_t at = size_t(row0 + m) * p.ldy + nb * 128 + (r >> 3) * 32 + u * 8 + (r & 7);
-    if (p.y_dtype == SHARQ_F32)
-      static_cast<float*>(p.Y)[at] = v;
-    else if (p.y_dtype == SHARQ_BF16)
-      static_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(v);
-    else
-      static_cast<__half*>(p.Y)[at] = __float2half_rn(v);
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h[4];
+      widen_bf16(reinterpret_cast<const uint32_t*>(&st.codes[i][lane])[q], h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = mul_bf16x2(h[j], q < 2 ? f[i][0] : f[i][1]);
+      a[i][0] = __byte_perm(h[0], h[1], 0x5410);
+      a[i][1] = __byte_perm(h[2], h[3], 0x5410);
+      a[i][2] = __byte_perm(h[0], h[1], 0x7632);
+      a[i][3] = __byte_perm(h[2], h[3], 0x7632);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (MT > 1 && m * 8 >= rows) break;
+      const uint4 b = load_x(m, q);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mma_bf16(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
+        mma_bf16(part[m][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (MT > 1 && m * 8 >= rows) break;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        acc.v[m][h][c] = fmaf(part[m][h][c], ref[2 * h + (c >> 1)], acc.v[m][h][c]);
   }
 }
 
-template <int MT, bool BF16>
-cudaError_t launch_view(const MatvecParams& p, ScaleView view, dim3 grid, cudaStream_t st) {
-  switch (view) {
-    case kE4M3x16:
-      return launch_dependent(matvec_kernel<MT, BF16, kE4M3x16>, grid, kWarps * 32, 0, st, p);
-    case kE4M3x32:
-      return launch_dependent(matvec_kernel<MT, BF16, kE4M3x32>, grid, kWarps * 32, 0, st, p);
-    default:
-      return launch_dependent(matvec_kernel<MT, BF16, kE8M0x32>, grid, kWarps * 32, 0, st, p);
-  }
+__device__ __forceinline__ void store_y(const MatvecParams& p, size_t at, float v) {
+  if (p.y_dtype == SHARQ_F32)
+    static_cast<float*>(p.Y)[at] = v;
+  else if (p.y_dtype == SHARQ_BF16)
+    static_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half*>(p.Y)[at] = __float2half_rn(v);
 }
 
+// First output of a lane-row: unit q (32 outputs), local output r.
+__device__ __forceinline__ int output_of(int q, int r) {
+  return (q >> 2) * 128 + (r >> 3) * 32 + (q & 3) * 8 + (r & 7);
+}
+
+// A warp's copies of the steps of a unit: the lane's codes and scale words.
+template <int VIEW>
+struct Source {
+  const uint8_t *codes, *scales;
+  __device__ __forceinline__ void set(const MatvecParams& p, int e, int q, int s) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int nb = q >> 2, u = q & 3, steps = p.K / kStepK;
+    codes = p.codes + size_t(e) * p.codes_stride + size_t(nb * 128 + u * 8 + g) * (p.K / 2) + t * 16 +
+            size_t(s) * 64;
+    scales = p.scales + size_t(e) * p.scales_stride + (size_t(nb) * steps + s) * kScaleStep<VIEW> +
+             (u * 8 + g) * 16 + (VIEW == kE4M3x16 ? (t >> 1) * 512 + (t & 1) * 8 : t * 4);
+  }
+  // copies a step and moves to the next one
+  __device__ __forceinline__ void fetch(uint32_t to_codes, uint32_t to_scales, size_t quarter) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) copy_async<16>(to_codes + i * 512, codes + i * quarter);
+    copy_async<VIEW == kE4M3x16 ? 8 : 4>(to_scales, scales);
+    codes += 64;
+    scales += kScaleStep<VIEW>;
+  }
+};
+// where the lane's scale words go in a Stage
+template <int VIEW>
+__device__ __forceinline__ uint32_t stage_scales(const Stage* st) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  return ptx::smem_u32(&st->scales[0][0]) +
+         (VIEW == kE4M3x16 ? (t >> 1) * 128 + g * 16 + (t & 1) * 8 : lane * 4);
+}
+
+constexpr int kWarps = 16;
+constexpr int kThreads = kWarps * 32;
+
+// Shared memory: rings; the warps' partial sums of their first and, for MT == 1, last unit
+// (for MT > 1 the last one's go into the warp's ring, which has run out by then); activations
+// [row][step], pitch 64 bytes over the steps' 256 (rows on other banks); their scalings; the
+// CTA's sums for the cluster; the experts' slots.
 template <int MT>
-cudaError_t launch_mt(const MatvecParams& p, bool bf16, ScaleView view, dim3 grid, cudaStream_t st) {
-  return bf16 ? launch_view<MT, true>(p, view, grid, st) : launch_view<MT, false>(p, view, grid, st);
+struct Layout {
+  int steps, rows, out_units, E;
+  // steps of weight per warp: one or two in flight beside the one in use
+  static constexpr int kRing = MT == 4 ? 2 : 3;
+  static constexpr int kRedRow = 8 * MT + 1;
+  static constexpr int kPart = kUnitRows * kRedRow;  // floats
+  static constexpr int kRingBytes = int(sizeof(Stage)) * kRing * kWarps;
+  static constexpr int kX = kRingBytes + kWarps * (MT == 1 ? 2 : 1) * kPart * 4;
+  static_assert(MT == 1 || kPart * 4 <= int(sizeof(Stage)) * kRing, "the last unit's sums fit in the ring");
+  __host__ __device__ int pitch() const { return steps * (kStepK * 2) + 64; }
+  __host__ __device__ int undo() const { return kX + rows * pitch(); }
+  __host__ __device__ int out() const { return undo() + steps * 8 * MT * 4; }
+  __host__ __device__ int table() const { return out() + out_units * rows * kUnitRows * 4; }
+  __host__ __device__ int bytes() const { return table() + (E > 0 ? (E + 1) * 4 : 0); }
+};
+
+template <int MT, bool BF16, int VIEW>
+__global__ void __launch_bounds__(kThreads, 1)
+matvec_kernel(const MatvecParams p) {
+  typedef Layout<MT> L;
+  constexpr int kRing = L::kRing;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int s_wide;
+  const int all_steps = p.K / kStepK, S = p.splits;
+  const int rank = S > 1 ? int(blockIdx.x) % S : 0;
+  const int cluster = S > 1 ? int(blockIdx.x) / S : int(blockIdx.x);
+  const int clusters = S > 1 ? int(gridDim.x) / S : int(gridDim.x);
+  const int s_begin = all_steps * rank / S, steps = all_steps * (rank + 1) / S - s_begin;
+  const L lay{(all_steps + S - 1) / S, p.x_rows, p.out_units, p.E};
+  // a warp's sums of its share's first unit (which 0) or last (1)
+  auto part_of = [&](int w, int which) {
+    if (MT == 1) return reinterpret_cast<float*>(smem + L::kRingBytes) + (w * 2 + which) * L::kPart;
+    return which == 0 ? reinterpret_cast<float*>(smem + L::kRingBytes) + w * L::kPart
+                      : reinterpret_cast<float*>(smem + w * (int(sizeof(Stage)) * kRing));
+  };
+  uint8_t* const s_x = smem + L::kX;
+  float* const s_undo = reinterpret_cast<float*>(smem + lay.undo());
+  float* const s_out = reinterpret_cast<float*>(smem + lay.out());
+  int* const s_table = reinterpret_cast<int*>(smem + lay.table());  // [E + 1] slots before each expert
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int units = p.N / kUnitRows;  // per slot
+  const size_t quarter = size_t(32) * (p.K / 2);
+
+  if (p.E > 0) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    if (warp == 0) {
+      int before = 0;
+      for (int base = 0; base < p.E; base += 32) {
+        const int e = base + lane;
+        const int rows = e < p.E ? p.offsets[e + 1] - p.offsets[e] : 0;
+        int incl = (rows + 8 * MT - 1) / (8 * MT);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+          if (lane >= d) incl += v;
+        }
+        if (e < p.E) s_table[e + 1] = before + incl;
+        before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+      }
+      if (lane == 0) s_table[0] = 0;
+    }
+    __syncthreads();
+  }
+  const int slots = p.E > 0 ? s_table[p.E] : (p.M + 8 * MT - 1) / (8 * MT);
+  const long long all = (long long)slots * units;
+  const int first = int(all * cluster / clusters), last = int(all * (cluster + 1) / clusters);
+  auto expert_of = [&](int slot) {
+    if (p.E == 0) return 0;
+    int lo = 0, hi = p.E;  // the last e with table[e] <= slot
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_table[mid] <= slot) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+  // A phase: units of one slot, from `at`; in a cluster no more than there is room for sums.
+  auto phase_end = [&](int at, int slot) {
+    const int end = min(last, (slot + 1) * units);
+    return S > 1 ? min(end, at + p.out_units) : end;
+  };
+
+  // The weight's stream: phase after phase, this warp's share of the phase's (unit, step) list
+  // in unit-major order. For MT > 1 it stops at the end of a phase, whose sums take the rings'
+  // place.
+  Stage* const ring = reinterpret_cast<Stage*>(smem) + warp * kRing;
+  const uint32_t to_codes = ptx::smem_u32(&ring[0].codes[0][lane]), to_scales = stage_scales<VIEW>(ring);
+  Source<VIEW> src;
+  int f_next = first;       // unit that starts the next phase to fetch
+  int f_at = 0, f_end = 0;  // next step of the phase's list, end of this warp's share
+  int f_step = 0, f_unit = 0, f_e = 0;
+  auto fetch_phase = [&]() {
+    const int slot = f_next / units, end = phase_end(f_next, slot);
+    const unsigned n = unsigned(end - f_next) * unsigned(steps);
+    f_at = int(n * warp / kWarps);
+    f_end = int(n * (warp + 1) / kWarps);
+    if (f_at < f_end) {
+      const int unit = f_at / steps;
+      f_step = f_at - unit * steps;
+      f_unit = f_next - slot * units + unit;
+      f_e = expert_of(slot);
+      src.set(p, f_e, f_unit, s_begin + f_step);
+    }
+    f_next = end;
+  };
+  auto fetch = [&](int to) {
+    if (MT == 1)
+      while (f_at == f_end && f_next < last) fetch_phase();  // a share of a short phase may be empty
+    if (f_at < f_end) {
+      src.fetch(to_codes + to * uint32_t(sizeof(Stage)), to_scales + to * uint32_t(sizeof(Stage)), quarter);
+      ++f_at;
+      if (++f_step == steps && f_at < f_end) {
+        f_step = 0;
+        src.set(p, f_e, ++f_unit, s_begin);
+      }
+    }
+    copies_commit();
+  };
+  auto preload = [&]() {
+    if (MT > 1 && f_next < last) fetch_phase();
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) fetch(i);
+  };
+  if (p.E == 0 && !p.early) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+  }
+  preload();
+  if (p.E == 0 && p.early) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+  }
+
+  // The slot's activations, the 16-byte units of a step permuted: K unit 4 t + q lies at
+  // 4 q + t, so that a lane quad reads 64 bytes. Sixteen threads per (row, step), 8 K each.
+  auto stage_x = [&](int row0, int rows, bool convert) {
+    constexpr int kBatch = 4, kGroups = kThreads / 16;
+    const int group = threadIdx.x >> 4, c = threadIdx.x & 15;
+    int r = 0, s = group;  // next (row, step) of the group
+    while (s >= steps && r < rows) { s -= steps; ++r; }
+    const int group2 = group & ~1;  // the warp's other half may have one more
+    int left = rows * steps > group2 ? (rows * steps - group2 + kGroups - 1) / kGroups : 0;
+    while (left > 0) {
+      uint4 v[kBatch];
+      int at[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        at[b] = -1;
+        v[b] = make_uint4(0, 0, 0, 0);
+        if (b < left && r < rows) {
+          const int row = row0 + r;
+          v[b] = *reinterpret_cast<const uint4*>(
+              static_cast<const uint16_t*>(p.X) + size_t(p.order ? p.order[row] / p.k : row) * p.ldx +
+              size_t(s_begin + s) * kStepK + c * 8);
+          at[b] = s << 8 | r;
+          s += kGroups;
+          while (s >= steps && r < rows) { s -= steps; ++r; }
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (b >= left) break;  // the same in the whole warp
+        const int rr = at[b] & 255, ss = at[b] >> 8;
+        if (convert) {
+          float undo;
+          bool wide;
+          v[b] = scale_bf16(v[b], &undo, &wide);
+          if (c == 0 && at[b] >= 0) {
+            s_undo[ss * (8 * MT) + rr] = undo;
+            if (wide) s_wide = 1;
+          }
+        }
+        if (at[b] >= 0)
+          *reinterpret_cast<uint4*>(s_x + rr * lay.pitch() + ss * (kStepK * 2) +
+                                    ((c & 3) * 4 + (c >> 2)) * 16) = v[b];
+      }
+      left -= kBatch;
+    }
+  };
+
+  int pos = 0, slot = -1, e = 0, row0 = 0, rows = 0;
+  bool wide = false;
+  float scale = 0.f;
+  for (int at = first; at < last;) {
+    const int now = at / units, end = phase_end(at, now), base = at - now * units;
+    if (now != slot) {
+      slot = now;
+      e = expert_of(slot);
+      const int row_first = p.E > 0 ? p.offsets[e] : 0, row_last = p.E > 0 ? p.offsets[e + 1] : p.M;
+      row0 = row_first + (slot - (p.E > 0 ? s_table[e] : 0)) * 8 * MT;
+      rows = max(1, min(min(row_last, p.M) - row0, min(8 * MT, p.x_rows)));
+      scale = p.w_scale[size_t(e) * 4];
+      if (BF16) {
+        if (threadIdx.x == 0) s_wide = 0;
+        __syncthreads();
+      }
+      stage_x(row0, rows, BF16);
+      __syncthreads();
+      wide = BF16 && s_wide;
+      if (wide) {
+        __syncthreads();
+        stage_x(row0, rows, false);
+        __syncthreads();
+      }
+    }
+
+    // rows past the last read the first one's: their sums are never stored
+    const unsigned n = unsigned(end - at) * unsigned(steps);
+    const int i_begin = int(n * warp / kWarps), i_end = int(n * (warp + 1) / kWarps);
+    int unit = i_begin / steps;
+    for (int i = i_begin, which = 0; i < i_end; ++unit, which = 1) {
+      const int seg_end = min(i_end, (unit + 1) * steps);
+      const bool whole = i == unit * steps && seg_end == (unit + 1) * steps;
+      Acc<MT> acc;
+      acc.clear();
+      for (int ls = i - unit * steps; i < seg_end; ++i, ++ls) {
+        copies_wait<kRing - 2>();
+        __syncwarp();  // the scale words come from four lanes; the stage before has been read
+        fetch(pos == 0 ? kRing - 1 : pos - 1);
+        const uint8_t* x = s_x + ls * (kStepK * 2) + t * 16;
+        auto load_x = [&](int m, int q) {
+          const int r = m * 8 + g < rows ? m * 8 + g : 0;
+          return *reinterpret_cast<const uint4*>(x + r * lay.pitch() + q * 64);
+        };
+        if (BF16 && wide)
+          step_bf16<MT, VIEW>(acc, ring[pos], rows, load_x);
+        else
+          step_f16<MT, VIEW, BF16>(acc, ring[pos], rows, load_x, [&](int m) {
+            return *reinterpret_cast<const float2*>(s_undo + ls * (8 * MT) + m * 8 + 2 * t);
+          });
+        pos = pos + 1 == kRing ? 0 : pos + 1;
+      }
+      if (MT > 1) __syncwarp();  // the ring has been read
+      float* part = part_of(warp, which);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if (MT > 1 && m * 8 >= rows) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int r = (2 * h + (c >> 1)) * 8 + g, mm = m * 8 + 2 * t + (c & 1);
+            if (!whole)
+              part[r * L::kRedRow + mm] = acc.v[m][h][c];
+            else if (mm < rows) {
+              if (S > 1)
+                s_out[(unit * rows + mm) * kUnitRows + r] = acc.v[m][h][c];
+              else
+                store_y(p, size_t(row0 + mm) * p.ldy + output_of(base + unit, r), acc.v[m][h][c] * scale);
+            }
+          }
+      }
+    }
+    __syncthreads();
+
+    // units that several warps share, in the warps' order: a warp takes 32 outputs of a row
+    {
+      const int nu = end - at;
+      int u = warp, m = 0;
+      while (u >= nu && m < rows) { u -= nu; ++m; }
+      while (m < rows) {
+        // the warp that holds step i of the list is the last w with n * w / 16 <= i
+        const unsigned lo = unsigned(u) * unsigned(steps);
+        const int w0 = int(((lo + 1) * kWarps - 1) / n), w1 = int(((lo + steps) * kWarps - 1) / n);
+        if (w0 != w1) {
+          float v = part_of(w0, n * w0 / kWarps == lo ? 0 : 1)[lane * L::kRedRow + m];
+#pragma unroll 4
+          for (int w = w0 + 1; w <= w1; ++w) {
+            const float x = part_of(w, 0)[lane * L::kRedRow + m];
+            v += n * w / kWarps < n * (w + 1) / kWarps ? x : 0.f;  // a share may be empty
+          }
+          if (S > 1)
+            s_out[(u * rows + m) * kUnitRows + lane] = v;
+          else
+            store_y(p, size_t(row0 + m) * p.ldy + output_of(base + u, lane), v * scale);
+        }
+        u += kWarps;
+        while (u >= nu && m < rows) { u -= nu; ++m; }
+      }
+    }
+    if (S > 1) {
+      ptx::cluster_sync();
+      const int pairs = (end - at) * rows;
+      for (int i = rank * kWarps + warp; i < pairs; i += S * kWarps) {
+        const uint32_t a = ptx::smem_u32(s_out + i * kUnitRows + lane);
+        float v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          v[c] = 0.f;
+          if (c < S) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[c]) : "r"(ptx::mapa(a, uint32_t(c))));
+        }
+        float sum = v[0];
+#pragma unroll
+        for (int c = 1; c < 8; ++c) sum += v[c];
+        const int u = i / rows, m = i - u * rows;
+        store_y(p, size_t(row0 + m) * p.ldy + output_of(base + u, lane), sum * scale);
+      }
+      ptx::cluster_sync();  // no CTA writes its sums again, or leaves, while they are read
+    } else if (end < last) {
+      __syncthreads();  // the slot's activations and sums have been read
+    }
+    at = end;
+    if (MT > 1 && at < last) {
+      pos = 0;
+      preload();
+    }
+  }
+  copies_wait<0>();
+}
+
+// ------------------------------------------------------------------------------ launch
+
+constexpr int kMaxSmem = 227 * 1024 - 64;  // less the static part
+
+// Clusters of S CTAs, one CTA per SM, that the current device runs at once.
+template <typename Kernel>
+cudaError_t max_clusters(Kernel* kern, int S, int smem, int num_sms, int* out) {
+  static std::atomic<int> known[4];  // by log2 S; every kernel here takes a whole SM
+  const int i = S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3;
+  *out = S == 1 ? num_sms : known[i].load(std::memory_order_relaxed);
+  if (*out > 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(num_sms / S * S));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(S);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(out, kern, &cfg);
+  if (e != cudaSuccess) return e;
+  if (*out < 1) return cudaErrorInvalidConfiguration;
+  known[i].store(*out, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
+template <int MT, bool BF16, int VIEW>
+cudaError_t launch_mt(MatvecParams p, int num_sms, cudaStream_t st) {
+  // K over as few CTAs as let the activations fit, beside the sums of at least two units
+  const int steps = p.K / kStepK;
+  int S = 1;
+  for (;; S *= 2) {
+    if (S > 8 || S > steps) return cudaErrorInvalidConfiguration;  // excluded by launch_view
+    if (Layout<MT>{(steps + S - 1) / S, p.x_rows, S > 1 ? 2 : 0, p.E}.bytes() <= kMaxSmem) break;
+  }
+  p.splits = S;
+  p.out_units = 0;
+  Layout<MT> lay{(steps + S - 1) / S, p.x_rows, 0, p.E};
+  if (S > 1) {
+    p.out_units = (kMaxSmem - lay.bytes()) / (p.x_rows * kUnitRows * 4);
+    if (p.out_units > p.N / kUnitRows) p.out_units = p.N / kUnitRows;
+    lay.out_units = p.out_units;
+  }
+  auto* kern = matvec_kernel<MT, BF16, VIEW>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, lay.bytes());
+  if (e != cudaSuccess) return e;
+  int clusters = 0;
+  if ((e = max_clusters(kern, S, lay.bytes(), num_sms, &clusters)) != cudaSuccess) return e;
+  const long long units = (long long)(p.N / kUnitRows) * (p.E > 0 ? p.M : (p.M + 8 * MT - 1) / (8 * MT));
+  if (units < clusters) clusters = int(units);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(clusters * S));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = size_t(lay.bytes());
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(S);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = S > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <bool BF16, int VIEW>
+cudaError_t launch_view(MatvecParams p, int num_sms, cudaStream_t st) {
+  // Rows per slot: 8 to 32. An expert's rows are not known here, twice their mean stands for
+  // them.
+  const int per = p.E > 0 ? 2 * ((p.M + p.E - 1) / p.E) : p.M;
+  const int steps = p.K / kStepK, eighth = (steps + 7) / 8;
+  int mt = per <= 8 ? 1 : per <= 16 ? 2 : per <= 24 ? 3 : 4;
+  auto fits = [&](int m) {
+    const int rows = p.E == 0 && p.M < 8 * m ? p.M : 8 * m;
+    return (m == 4   ? Layout<4>{eighth, rows, 2, p.E}.bytes()
+            : m == 3 ? Layout<3>{eighth, rows, 2, p.E}.bytes()
+            : m == 2 ? Layout<2>{eighth, rows, 2, p.E}.bytes()
+                     : Layout<1>{eighth, rows, 2, p.E}.bytes()) <= kMaxSmem;
+  };
+  while (mt > 1 && !fits(mt)) --mt;
+  if (!fits(mt)) return cudaErrorInvalidConfiguration;  // K is bounded by the caller's checks
+  p.x_rows = p.E == 0 && p.M < 8 * mt ? p.M : 8 * mt;
+  switch (mt) {
+    case 1: return launch_mt<1, BF16, VIEW>(p, num_sms, st);
+    case 2: return launch_mt<2, BF16, VIEW>(p, num_sms, st);
+    case 3: return launch_mt<3, BF16, VIEW>(p, num_sms, st);
+    default: return launch_mt<4, BF16, VIEW>(p, num_sms, st);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_matvec(const MatvecParams& p, bool bf16, ScaleView view, cudaStream_t st) {
-  // rows per CTA: 8 or 32; an expert's rows are not known here, their mean stands for them
-  const int per = p.E > 0 ? (p.M + p.E - 1) / p.E : p.M;
-  const int chunk = per <= 8 ? 8 : 32;
-  const unsigned units = unsigned(p.N / kUnitRows);
-  unsigned chunks = unsigned((p.M + chunk - 1) / chunk);
-  // sum over experts of ceil(rows / chunk) <= experts with rows + M / chunk
-  if (p.E > 0) chunks = unsigned((p.E < p.M ? p.E : p.M) + p.M / chunk);
-  if (chunks > 65535u) return cudaErrorInvalidConfiguration;  // bounded by the caller's checks
-  const dim3 grid(units, chunks);
-  return chunk == 8 ? launch_mt<1>(p, bf16, view, grid, st) : launch_mt<4>(p, bf16, view, grid, st);
+cudaError_t launch_matvec(const MatvecParams& p, bool bf16, ScaleView view, int num_sms,
+                          cudaStream_t st) {
+  switch (view) {
+    case kE4M3x16:
+      return bf16 ? launch_view<true, kE4M3x16>(p, num_sms, st) : launch_view<false, kE4M3x16>(p, num_sms, st);
+    case kE4M3x32:
+      return bf16 ? launch_view<true, kE4M3x32>(p, num_sms, st) : launch_view<false, kE4M3x32>(p, num_sms, st);
+    default:
+      return bf16 ? launch_view<true, kE8M0x32>(p, num_sms, st) : launch_view<false, kE8M0x32>(p, num_sms, st);
+  }
 }
 
 }  // namespace sharq
