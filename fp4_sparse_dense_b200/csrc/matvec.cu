@@ -380,6 +380,24 @@ __device__ __forceinline__ void step_bf16(Acc<MT>& acc, const Stage& st, int row
   }
 }
 
+template <int Y>
+struct YType;
+template <>
+struct YType<SHARQ_F32> {
+  typedef float T;
+  static __device__ __forceinline__ T of(float v) { return v; }
+};
+template <>
+struct YType<SHARQ_BF16> {
+  typedef __nv_bfloat16 T;
+  static __device__ __forceinline__ T of(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct YType<SHARQ_F16> {
+  typedef __half T;
+  static __device__ __forceinline__ T of(float v) { return __float2half_rn(v); }
+};
+
 __device__ __forceinline__ void store_y(const MatvecParams& p, size_t at, float v) {
   if (p.y_dtype == SHARQ_F32)
     static_cast<float*>(p.Y)[at] = v;
@@ -387,6 +405,22 @@ __device__ __forceinline__ void store_y(const MatvecParams& p, size_t at, float 
     static_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(v);
   else
     static_cast<__half*>(p.Y)[at] = __float2half_rn(v);
+}
+
+// A lane's sums of a whole unit -> Y, at the lane's first output and row.
+template <int MT, int Y>
+__device__ __forceinline__ void store_unit(const MatvecParams& p, const Acc<MT>& acc, size_t at,
+                                           int rows_left, float scale) {
+  typedef typename YType<Y>::T T;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (m * 8 + j < rows_left) {
+        T* y = static_cast<T*>(p.Y) + at + size_t(m * 8 + j) * p.ldy;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i * 32] = YType<Y>::of(acc.v[m][i >> 1][(i & 1) * 2 + j] * scale);
+      }
 }
 
 // First output of a lane-row: unit q (32 outputs), local output r.
@@ -430,6 +464,7 @@ constexpr int kThreads = kWarps * 32;
 // (for MT > 1 the last one's go into the warp's ring, which has run out by then); activations
 // [row][step], pitch 64 bytes over the steps' 256 (rows on other banks); their scalings; the
 // CTA's sums for the cluster; the experts' slots.
+constexpr int kMaxUnits = 64;  // of a phase
 template <int MT>
 struct Layout {
   int steps, rows, out_units, E;
@@ -454,6 +489,7 @@ matvec_kernel(const MatvecParams p) {
   constexpr int kRing = L::kRing;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int s_wide;
+  __shared__ int s_span[kMaxUnits];  // warps that share a unit: first | last << 8 | (first one's which) << 16
   const int all_steps = p.K / kStepK, S = p.splits;
   const int rank = S > 1 ? int(blockIdx.x) % S : 0;
   const int cluster = S > 1 ? int(blockIdx.x) / S : int(blockIdx.x);
@@ -511,8 +547,7 @@ matvec_kernel(const MatvecParams p) {
   };
   // A phase: units of one slot, from `at`; in a cluster no more than there is room for sums.
   auto phase_end = [&](int at, int slot) {
-    const int end = min(last, (slot + 1) * units);
-    return S > 1 ? min(end, at + p.out_units) : end;
+    return min(min(last, (slot + 1) * units), at + (S > 1 ? p.out_units : kMaxUnits));
   };
 
   // The weight's stream: phase after phase, this warp's share of the phase's (unit, step) list
@@ -639,8 +674,14 @@ matvec_kernel(const MatvecParams p) {
       }
     }
 
-    // rows past the last read the first one's: their sums are never stored
     const unsigned n = unsigned(end - at) * unsigned(steps);
+    if (int(threadIdx.x) < end - at) {
+      // the warp that holds step i of the list is the last w with n * w / 16 <= i
+      const unsigned lo = threadIdx.x * unsigned(steps);
+      const unsigned w0 = ((lo + 1) * kWarps - 1) / n, w1 = ((lo + steps) * kWarps - 1) / n;
+      s_span[threadIdx.x] = int(w0 | w1 << 8 | (n * w0 / kWarps == lo ? 0u : 1u) << 16);
+    }
+    // rows past the last read the first one's: their sums are never stored
     const int i_begin = int(n * warp / kWarps), i_end = int(n * (warp + 1) / kWarps);
     int unit = i_begin / steps;
     for (int i = i_begin, which = 0; i < i_end; ++unit, which = 1) {
@@ -666,24 +707,36 @@ matvec_kernel(const MatvecParams p) {
         pos = pos + 1 == kRing ? 0 : pos + 1;
       }
       if (MT > 1) __syncwarp();  // the ring has been read
-      float* part = part_of(warp, which);
+      if (!whole) {
+        float* part = part_of(warp, which) + g * L::kRedRow + 2 * t;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        if (MT > 1 && m * 8 >= rows) break;
+        for (int m = 0; m < MT; ++m) {
+          if (MT > 1 && m * 8 >= rows) break;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int r = (2 * h + (c >> 1)) * 8 + g, mm = m * 8 + 2 * t + (c & 1);
-            if (!whole)
-              part[r * L::kRedRow + mm] = acc.v[m][h][c];
-            else if (mm < rows) {
-              if (S > 1)
-                s_out[(unit * rows + mm) * kUnitRows + r] = acc.v[m][h][c];
-              else
-                store_y(p, size_t(row0 + mm) * p.ldy + output_of(base + unit, r), acc.v[m][h][c] * scale);
+            for (int c = 0; c < 4; ++c)
+              part[(2 * h + (c >> 1)) * 8 * L::kRedRow + m * 8 + (c & 1)] = acc.v[m][h][c];
+        }
+      } else if (S > 1) {
+        float* out = s_out + (unit * rows + 2 * t) * kUnitRows + g;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (m * 8 + j < rows - 2 * t) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                out[(m * 8 + j) * kUnitRows + i * 8] = acc.v[m][i >> 1][(i & 1) * 2 + j];
             }
-          }
+      } else {
+        const size_t y = size_t(row0 + 2 * t) * p.ldy + output_of(base + unit, g);
+        if (p.y_dtype == SHARQ_BF16)
+          store_unit<MT, SHARQ_BF16>(p, acc, y, rows - 2 * t, scale);
+        else if (p.y_dtype == SHARQ_F16)
+          store_unit<MT, SHARQ_F16>(p, acc, y, rows - 2 * t, scale);
+        else
+          store_unit<MT, SHARQ_F32>(p, acc, y, rows - 2 * t, scale);
       }
     }
     __syncthreads();
@@ -694,15 +747,23 @@ matvec_kernel(const MatvecParams p) {
       int u = warp, m = 0;
       while (u >= nu && m < rows) { u -= nu; ++m; }
       while (m < rows) {
-        // the warp that holds step i of the list is the last w with n * w / 16 <= i
-        const unsigned lo = unsigned(u) * unsigned(steps);
-        const int w0 = int(((lo + 1) * kWarps - 1) / n), w1 = int(((lo + steps) * kWarps - 1) / n);
+        const int span = s_span[u], w0 = span & 255, w1 = (span >> 8) & 255;
         if (w0 != w1) {
-          float v = part_of(w0, n * w0 / kWarps == lo ? 0 : 1)[lane * L::kRedRow + m];
-#pragma unroll 4
-          for (int w = w0 + 1; w <= w1; ++w) {
-            const float x = part_of(w, 0)[lane * L::kRedRow + m];
-            v += n * w / kWarps < n * (w + 1) / kWarps ? x : 0.f;  // a share may be empty
+          float v = part_of(w0, span >> 16)[lane * L::kRedRow + m];
+          constexpr int kNext = (MT == 1 ? 2 : 1) * L::kPart;
+          const float* next = part_of(w0 + 1, 0) + lane * L::kRedRow + m;
+          if (n >= unsigned(kWarps)) {
+            for (int w = w1 - w0; w > 0; w -= 4, next += 4 * kNext) {
+              const float x0 = next[0], x1 = w > 1 ? next[kNext] : 0.f, x2 = w > 2 ? next[2 * kNext] : 0.f,
+                          x3 = w > 3 ? next[3 * kNext] : 0.f;
+              v += x0;
+              v += x1;
+              v += x2;
+              v += x3;
+            }
+          } else {  // fewer steps than warps: some shares are empty
+            for (int w = w0 + 1; w <= w1; ++w, next += kNext)
+              if (n * unsigned(w) / kWarps < n * unsigned(w + 1) / kWarps) v += *next;
           }
           if (S > 1)
             s_out[(u * rows + m) * kUnitRows + lane] = v;
@@ -716,7 +777,9 @@ matvec_kernel(const MatvecParams p) {
     if (S > 1) {
       ptx::cluster_sync();
       const int pairs = (end - at) * rows;
-      for (int i = rank * kWarps + warp; i < pairs; i += S * kWarps) {
+      int u = 0, m = rank * kWarps + warp;
+      for (int i = m; i < pairs; i += S * kWarps, m += S * kWarps) {
+        while (m >= rows) { m -= rows; ++u; }
         const uint32_t a = ptx::smem_u32(s_out + i * kUnitRows + lane);
         float v[8];
 #pragma unroll
@@ -727,7 +790,6 @@ matvec_kernel(const MatvecParams p) {
         float sum = v[0];
 #pragma unroll
         for (int c = 1; c < 8; ++c) sum += v[c];
-        const int u = i / rows, m = i - u * rows;
         store_y(p, size_t(row0 + m) * p.ldy + output_of(base + u, lane), sum * scale);
       }
       ptx::cluster_sync();  // no CTA writes its sums again, or leaves, while they are read

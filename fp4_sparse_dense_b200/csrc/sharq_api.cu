@@ -771,9 +771,8 @@ sharq_status sharq_matvec(const void* X, size_t ldx, int32_t M, sharq_dtype dtyp
   DeviceInfo d;
   if ((s = device_info(&d)) != SHARQ_OK || M == 0) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  s = from_cuda(launch_matvec(p, dtype == SHARQ_BF16, view, d.num_sms, st));
-  note_launch(d, st, s == SHARQ_OK);
-  return s;
+  p.early = note_launch(d, st, true) ? 1 : 0;
+  return from_cuda(launch_matvec(p, dtype == SHARQ_BF16, view, d.num_sms, st));
 }
 
 sharq_status sharq_expert_matvec(const void* X, size_t ldx, int32_t gather, sharq_dtype dtype,
