@@ -1,6 +1,7 @@
 // Declarations shared by the translation units of the 16-bit-activation operators
 // (matvec.cu, tokens.cu) and the C ABI (sharq_api.cu). Not part of the ABI.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -35,7 +36,7 @@ struct MatvecParams {
 };
 
 cudaError_t launch_matvec(const MatvecParams& p, bool bf16, ScaleView view, int num_sms,
-                          cudaStream_t st);
+                          unsigned long long ctx, cudaStream_t st);
 
 struct SortParams {
   const void* experts;  // [T * k] int32 or int64
@@ -45,7 +46,7 @@ struct SortParams {
   int32_t* order;
   int32_t* place;
 };
-cudaError_t launch_sort(const SortParams& p, cudaStream_t st);
+cudaError_t launch_sort(const SortParams& p, unsigned long long ctx, cudaStream_t st);
 
 // Rows moved between token order and expert order. H elements of `dtype` per row; every
 // matrix has a row pitch in elements.
@@ -62,6 +63,18 @@ struct RowsParams {
 };
 enum RowsOp { kGather = 0, kCombine = 1, kCombineGrad = 2 };
 cudaError_t launch_rows(const RowsParams& p, RowsOp op, int dtype, cudaStream_t st);
+
+// Allows `kern` up to `smem` bytes of dynamic shared memory in context `ctx`; `done` is the
+// kernel's own record of the last context that this was done for.
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel* kern, int smem, unsigned long long ctx,
+                              std::atomic<unsigned long long>* done) {
+  if (done->load(std::memory_order_acquire) == ctx) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) done->store(ctx, std::memory_order_release);
+  return e;
+}
 
 // Launches `kern` with the programmatic-stream-serialization attribute: it may start while
 // the kernel before it on the stream finishes, and waits (griddepcontrol.wait) before it

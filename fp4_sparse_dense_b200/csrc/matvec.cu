@@ -807,7 +807,7 @@ matvec_kernel(const MatvecParams p) {
 
 // ------------------------------------------------------------------------------ launch
 
-constexpr int kMaxSmem = 227 * 1024 - 64;  // less the static part
+constexpr int kMaxSmem = 226 * 1024;  // 227 KB less the static part
 
 // Clusters of S CTAs, one CTA per SM, that the current device runs at once.
 template <typename Kernel>
@@ -835,7 +835,7 @@ cudaError_t max_clusters(Kernel* kern, int S, int smem, int num_sms, int* out) {
 }
 
 template <int MT, bool BF16, int VIEW>
-cudaError_t launch_mt(MatvecParams p, int num_sms, cudaStream_t st) {
+cudaError_t launch_mt(MatvecParams p, int num_sms, unsigned long long ctx, cudaStream_t st) {
   // K over as few CTAs as let the activations fit, beside the sums of at least two units
   const int steps = p.K / kStepK;
   int S = 1;
@@ -852,7 +852,8 @@ cudaError_t launch_mt(MatvecParams p, int num_sms, cudaStream_t st) {
     lay.out_units = p.out_units;
   }
   auto* kern = matvec_kernel<MT, BF16, VIEW>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, lay.bytes());
+  static std::atomic<unsigned long long> done{~0ull};
+  cudaError_t e = allow_smem(kern, kMaxSmem, ctx, &done);
   if (e != cudaSuccess) return e;
   int clusters = 0;
   if ((e = max_clusters(kern, S, lay.bytes(), num_sms, &clusters)) != cudaSuccess) return e;
@@ -876,7 +877,7 @@ cudaError_t launch_mt(MatvecParams p, int num_sms, cudaStream_t st) {
 }
 
 template <bool BF16, int VIEW>
-cudaError_t launch_view(MatvecParams p, int num_sms, cudaStream_t st) {
+cudaError_t launch_view(MatvecParams p, int num_sms, unsigned long long ctx, cudaStream_t st) {
   // Rows per slot: 8 to 32. An expert's rows are not known here, twice their mean stands for
   // them.
   const int per = p.E > 0 ? 2 * ((p.M + p.E - 1) / p.E) : p.M;
@@ -893,24 +894,24 @@ cudaError_t launch_view(MatvecParams p, int num_sms, cudaStream_t st) {
   if (!fits(mt)) return cudaErrorInvalidConfiguration;  // K is bounded by the caller's checks
   p.x_rows = p.E == 0 && p.M < 8 * mt ? p.M : 8 * mt;
   switch (mt) {
-    case 1: return launch_mt<1, BF16, VIEW>(p, num_sms, st);
-    case 2: return launch_mt<2, BF16, VIEW>(p, num_sms, st);
-    case 3: return launch_mt<3, BF16, VIEW>(p, num_sms, st);
-    default: return launch_mt<4, BF16, VIEW>(p, num_sms, st);
+    case 1: return launch_mt<1, BF16, VIEW>(p, num_sms, ctx, st);
+    case 2: return launch_mt<2, BF16, VIEW>(p, num_sms, ctx, st);
+    case 3: return launch_mt<3, BF16, VIEW>(p, num_sms, ctx, st);
+    default: return launch_mt<4, BF16, VIEW>(p, num_sms, ctx, st);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_matvec(const MatvecParams& p, bool bf16, ScaleView view, int num_sms,
-                          cudaStream_t st) {
+                          unsigned long long ctx, cudaStream_t st) {
   switch (view) {
     case kE4M3x16:
-      return bf16 ? launch_view<true, kE4M3x16>(p, num_sms, st) : launch_view<false, kE4M3x16>(p, num_sms, st);
+      return bf16 ? launch_view<true, kE4M3x16>(p, num_sms, ctx, st) : launch_view<false, kE4M3x16>(p, num_sms, ctx, st);
     case kE4M3x32:
-      return bf16 ? launch_view<true, kE4M3x32>(p, num_sms, st) : launch_view<false, kE4M3x32>(p, num_sms, st);
+      return bf16 ? launch_view<true, kE4M3x32>(p, num_sms, ctx, st) : launch_view<false, kE4M3x32>(p, num_sms, ctx, st);
     default:
-      return bf16 ? launch_view<true, kE8M0x32>(p, num_sms, st) : launch_view<false, kE8M0x32>(p, num_sms, st);
+      return bf16 ? launch_view<true, kE8M0x32>(p, num_sms, ctx, st) : launch_view<false, kE8M0x32>(p, num_sms, ctx, st);
   }
 }
 

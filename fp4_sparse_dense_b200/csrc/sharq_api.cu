@@ -92,14 +92,20 @@ std::unordered_map<StreamKey, StreamState, StreamKeyHash> g_streams;
 std::unordered_map<unsigned long long, int> g_next_slot;  // context id -> next slot to hand out
 
 sharq_status device_info(DeviceInfo* out) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return SHARQ_ERR_CUDA;
   unsigned long long ctx = 0;
   if (current_context_id(&ctx) != SHARQ_OK) return SHARQ_ERR_CUDA;
+  // the calling thread's last context: its facts never change
+  static thread_local DeviceInfo last;
+  if (last.ok && last.ctx_id == ctx) {
+    *out = last;
+    return SHARQ_OK;
+  }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SHARQ_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_mu);
   auto it = g_dev.find(ctx);
   if (it != g_dev.end()) {
-    *out = it->second;
+    *out = last = it->second;
     return out->ok ? SHARQ_OK : SHARQ_ERR_ARCH;
   }
   DeviceInfo d;
@@ -120,7 +126,7 @@ sharq_status device_info(DeviceInfo* out) {
     d.status_taken = static_cast<unsigned int*>(t);
   }
   g_dev[ctx] = d;
-  *out = d;
+  *out = last = d;
   return d.ok ? SHARQ_OK : SHARQ_ERR_ARCH;
 }
 
@@ -772,7 +778,7 @@ sharq_status sharq_matvec(const void* X, size_t ldx, int32_t M, sharq_dtype dtyp
   if ((s = device_info(&d)) != SHARQ_OK || M == 0) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   p.early = note_launch(d, st, true) ? 1 : 0;
-  return from_cuda(launch_matvec(p, dtype == SHARQ_BF16, view, d.num_sms, st));
+  return from_cuda(launch_matvec(p, dtype == SHARQ_BF16, view, d.num_sms, d.ctx_id, st));
 }
 
 sharq_status sharq_expert_matvec(const void* X, size_t ldx, int32_t gather, sharq_dtype dtype,
@@ -796,7 +802,7 @@ sharq_status sharq_expert_matvec(const void* X, size_t ldx, int32_t gather, shar
   DeviceInfo d;
   if ((s = device_info(&d)) != SHARQ_OK || p.M == 0) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  s = from_cuda(launch_matvec(p, dtype == SHARQ_BF16, view, d.num_sms, st));
+  s = from_cuda(launch_matvec(p, dtype == SHARQ_BF16, view, d.num_sms, d.ctx_id, st));
   note_launch(d, st, s == SHARQ_OK);
   return s;
 }
@@ -830,7 +836,7 @@ sharq_status sharq_sort_tokens(const void* experts, int32_t id_bits, const sharq
   p.offsets = t->offsets;
   p.order = t->order;
   p.place = t->place;
-  s = from_cuda(launch_sort(p, st));
+  s = from_cuda(launch_sort(p, d.ctx_id, st));
   note_launch(d, st, s == SHARQ_OK);
   if (s != SHARQ_OK || !move) return s;
   return from_cuda(launch_rows(r, kGather, dtype, st));

@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxExperts = 1024;
 
 __device__ __forceinline__ int expert_of(const SortParams& p, int a) {
   const long long id = p.ids64 ? static_cast<const long long*>(p.experts)[a]
@@ -259,13 +260,11 @@ cudaError_t launch_rows_op(const RowsParams& p, int dtype, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_sort(const SortParams& p, cudaStream_t st) {
+cudaError_t launch_sort(const SortParams& p, unsigned long long ctx, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{~0ull};
+  const cudaError_t e = allow_smem(sort_kernel, kSortWarps * (kMaxExperts + 1) * 4, ctx, &done);
+  if (e != cudaSuccess) return e;
   const size_t smem = size_t(kSortWarps) * size_t(p.E + 1) * sizeof(int32_t);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
-  }
   return launch_dependent(sort_kernel, dim3(1), kSortThreads, smem, st, p);
 }
 

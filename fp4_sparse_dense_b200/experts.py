@@ -15,22 +15,29 @@ or TypeError here, or SharqError with the C status.
 """
 from __future__ import annotations
 
-import ctypes
+from ctypes import byref
 from dataclasses import dataclass
 
 import torch
 
-from . import (BF16, Config, F16, F32, QuantWeight, _CStructCache, _ptr, _stream,
-               check, quantize_weight)
-from . import _abi
-from ._abi import sharq_expert_weights, sharq_tokens, sharq_weight_bytes, sharq_weight_sizes
+from . import (BF16, Config, F16, F32, QuantWeight, _CStructCache, _ptr, check,
+               quantize_weight)
+from ._abi import (
+    sharq_combine_tokens as _combine_tokens, sharq_combine_tokens_backward as _combine_tokens_backward,
+    sharq_expert_matvec as _expert_matvec, sharq_expert_weights, sharq_matvec as _matvec,
+    sharq_sort_tokens as _sort_tokens, sharq_tokens, sharq_weight_bytes, sharq_weight_sizes,
+)
 
 _DTYPE = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
 
 
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _elsewhere(device, stream) -> bool:
     """Whether the call has to switch to `stream` or to the tensors' device first."""
-    return stream is not None or device.index != torch.cuda.current_device()
+    return stream is not None or device.index != _current_device()
 
 
 def _on(device, stream):
@@ -68,27 +75,37 @@ def _code16(name, x) -> int:
 def _matrix(name, x, rows, cols, device):
     """Checks a [rows, cols] matrix with unit column stride and returns its row pitch."""
     _cuda(name, x, device)
-    if x.dim() != 2 or x.shape[0] != rows or x.shape[1] != cols:
+    if x.dim() != 2 or x.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(x.shape)}")
-    ld = x.stride(0)
+    if x.is_contiguous():
+        return cols
+    ld, unit = x.stride()
     if rows <= 1:
-        ld = max(ld, cols)
-    if (cols > 1 and x.stride(1) != 1) or ld < cols:
+        ld = cols
+    if (cols > 1 and unit != 1) or ld < cols:
         raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
     return ld
 
 
 def _readable(name, x, align16=False):
-    """An input matrix as the kernels read it: unit column stride, rows that do not overlap
-    (an expanded or transposed view is copied), and for the products 16-byte rows."""
+    """An input matrix as the kernels read it, and its row pitch: unit column stride, rows that
+    do not overlap (an expanded or transposed view is copied), and for the products 16-byte
+    rows."""
     if x.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got {list(x.shape)}")
     rows, cols = x.shape
-    ld = x.stride(0)
-    ok = (cols <= 1 or x.stride(1) == 1) and (rows <= 1 or ld >= cols)
-    if align16 and ok:
-        ok = (rows <= 1 or ld % 8 == 0) and x.data_ptr() % 16 == 0
-    return x if ok else x.clone(memory_format=torch.contiguous_format)
+    if x.is_contiguous():
+        ld, ok = cols, True
+    else:
+        ld, unit = x.stride()
+        if rows <= 1:
+            ld = cols
+        ok = (cols <= 1 or unit == 1) and ld >= cols
+    if align16 and (ld % 8 or x.data_ptr() % 16):
+        ok = False
+    if ok:
+        return x, rows, cols, ld
+    return x.clone(memory_format=torch.contiguous_format), rows, cols, cols
 
 
 # ------------------------------------------------------------------ the few-row product
@@ -107,20 +124,21 @@ def matvec(X, w: QuantWeight, out=None, out_dtype=None, stream=None):
         with _on(device, stream):
             return matvec(X, w, out, out_dtype)
     code = _code16("X", X)
-    X = _readable("X", X, align16=True)
-    M = X.shape[0]
-    ldx = _matrix("X", X, M, w.K, device)
-    _cuda("w.codes", w.codes, device)
+    X, M, K, ldx = _readable("X", X, align16=True)
+    N = w.N
+    if K != w.K:
+        raise ValueError(f"X must be [M, {w.K}], got {list(X.shape)}")
+    if w.codes.device != device:
+        raise ValueError(f"w is on {w.codes.device}, expected {device}")
     if out is None:
-        out = torch.empty(M, w.N, dtype=out_dtype or X.dtype, device=device)
-        ldy = w.N
+        out = torch.empty((M, N), dtype=out_dtype or X.dtype, device=device)
+        ldy = N
     else:
-        ldy = _matrix("out", out, M, w.N, device)
+        ldy = _matrix("out", out, M, N, device)
     if M == 0:
         return out
-    check(_abi.sharq_matvec(X.data_ptr(), (ldx + 7) & ~7 if M == 1 else ldx, M, code,
-                            ctypes.byref(w.c()), out.data_ptr(), ldy, _code("out", out),
-                            _stream(None, device)))
+    check(_matvec(X.data_ptr(), ldx, M, code, byref(w.c()), out.data_ptr(), ldy,
+                  _code("out", out), _current_stream(device.index)))
     return out
 
 
@@ -154,7 +172,7 @@ class ExpertWeights(_CStructCache):
 
     def _bytes(self) -> sharq_weight_bytes:
         sz = sharq_weight_bytes()
-        check(sharq_weight_sizes(self.K, self.N, self.cfg.c(), ctypes.byref(sz)))
+        check(sharq_weight_sizes(self.K, self.N, self.cfg.c(), byref(sz)))
         return sz
 
     def expert(self, e: int) -> QuantWeight:
@@ -182,7 +200,7 @@ def quantize_experts(W, cfg: Config = Config(), stream=None) -> ExpertWeights:
             return quantize_experts(W, cfg)
     E, K, N = W.shape
     one = sharq_weight_bytes()
-    check(sharq_weight_sizes(K, N, cfg.c(), ctypes.byref(one)))
+    check(sharq_weight_sizes(K, N, cfg.c(), byref(one)))
 
     def stack(n):
         return torch.empty(E, n, dtype=torch.uint8, device=W.device) if n else None
@@ -218,6 +236,19 @@ class SortedTokens(_CStructCache):
                             self.T, self.k, self.E)
 
 
+def _empty_tokens(T, k, E, device) -> SortedTokens:
+    """SortedTokens over one new buffer; its parts fit by construction, so the C struct is made
+    here without the checks of _make_c."""
+    n = T * k
+    plan = torch.empty(2 * n + E + 1, dtype=torch.int32, device=device)
+    order, place, offsets = plan.split_with_sizes((n, n, E + 1))
+    t = object.__new__(SortedTokens)
+    p = plan.data_ptr()
+    t.__dict__.update(offsets=offsets, order=order, place=place.view(T, k), T=T, k=k, E=E,
+                      _c=sharq_tokens(p + 8 * n, p, p + 4 * n, T, k, E))
+    return t
+
+
 def sort_tokens(experts, num_experts: int, X=None, rows=None, out: SortedTokens | None = None,
                 stream=None):
     """Stable order of the assignments `experts` [T, k] (int32 or int64; an id outside
@@ -238,11 +269,10 @@ def sort_tokens(experts, num_experts: int, X=None, rows=None, out: SortedTokens 
     else:
         raise TypeError(f"unsupported dtype {experts.dtype} of experts (need int32 or int64)")
     T, k = experts.shape
-    experts = experts.contiguous()
+    if not experts.is_contiguous():
+        experts = experts.contiguous()
     if out is None:
-        plan = torch.empty(2 * T * k + num_experts + 1, dtype=torch.int32, device=device)
-        order, place, offsets = plan.split((T * k, T * k, num_experts + 1))
-        out = SortedTokens(offsets, order, place.view(T, k), T, k, num_experts)
+        out = _empty_tokens(T, k, num_experts, device)
     elif (out.T, out.k, out.E) != (T, k, num_experts):
         raise ValueError(f"out is for T, k, E = {out.T}, {out.k}, {out.E}")
     else:
@@ -250,12 +280,13 @@ def sort_tokens(experts, num_experts: int, X=None, rows=None, out: SortedTokens 
     x_ptr = rows_ptr = None
     ldx = ld_rows = H = code = 0
     if X is not None:
-        X = _readable("X", X)
-        H = X.shape[1]
-        ldx = _matrix("X", X, T, H, device)
+        _cuda("X", X, device)
+        X, n, H, ldx = _readable("X", X)
+        if n != T:
+            raise ValueError(f"X must be [{T}, H], got {list(X.shape)}")
         code = _code("X", X)
         if rows is None:
-            rows = torch.empty(T * k, H, dtype=X.dtype, device=device)
+            rows = torch.empty((T * k, H), dtype=X.dtype, device=device)
             ld_rows = H
         else:
             ld_rows = _matrix("rows", rows, T * k, H, device)
@@ -264,8 +295,8 @@ def sort_tokens(experts, num_experts: int, X=None, rows=None, out: SortedTokens 
         x_ptr, rows_ptr = X.data_ptr(), rows.data_ptr()
     elif rows is not None:
         raise ValueError("rows without X")
-    check(_abi.sharq_sort_tokens(experts.data_ptr(), bits, ctypes.byref(out.c()), x_ptr, ldx, H,
-                                 code, rows_ptr, ld_rows, _stream(None, device)))
+    check(_sort_tokens(experts.data_ptr(), bits, byref(out.c()), x_ptr, ldx, H, code, rows_ptr,
+                       ld_rows, _current_stream(device.index)))
     return out, rows
 
 
@@ -288,33 +319,32 @@ def expert_matvec(X, w: ExpertWeights, tokens: SortedTokens, gather: bool = Fals
     if w.E != tokens.E:
         raise ValueError(f"{w.E} expert weights, tokens sorted over {tokens.E}")
     code = _code16("X", X)
-    X = _readable("X", X, align16=True)
     n = tokens.T * tokens.k
-    rows = tokens.T if gather else n
-    ldx = _matrix("X", X, rows, w.K, device)
-    _cuda("w.codes", w.codes, device)
-    _cuda("tokens.offsets", tokens.offsets, device)
+    X, rows, K, ldx = _readable("X", X, align16=True)
+    if rows != (tokens.T if gather else n) or K != w.K:
+        raise ValueError(f"X must be [{tokens.T if gather else n}, {w.K}], got {list(X.shape)}")
+    if w.codes.device != device or tokens.offsets.device != device:
+        raise ValueError(f"w is on {w.codes.device}, tokens on {tokens.offsets.device}, expected {device}")
     if out is None:
-        out = torch.empty(n, w.N, dtype=out_dtype or X.dtype, device=device)
+        out = torch.empty((n, w.N), dtype=out_dtype or X.dtype, device=device)
         ldy = w.N
     else:
         ldy = _matrix("out", out, n, w.N, device)
     if n == 0:
         return out
-    check(_abi.sharq_expert_matvec(X.data_ptr(), (ldx + 7) & ~7 if rows == 1 else ldx,
-                                   1 if gather else 0, code, ctypes.byref(tokens.c()),
-                                   ctypes.byref(w.c()), out.data_ptr(), ldy, _code("out", out),
-                                   _stream(None, device)))
+    check(_expert_matvec(X.data_ptr(), ldx, 1 if gather else 0, code, byref(tokens.c()),
+                         byref(w.c()), out.data_ptr(), ldy, _code("out", out),
+                         _current_stream(device.index)))
     return out
 
 
 def _weights(weights, tokens, device):
     _cuda("weights", weights, device)
-    if weights.dtype != torch.float32:
+    if weights.dtype is not torch.float32:
         raise TypeError(f"unsupported dtype {weights.dtype} of weights (need float32)")
-    if weights.numel() != tokens.T * tokens.k or weights.shape[0] != tokens.T:
+    if weights.shape != (tokens.T, tokens.k):
         raise ValueError(f"weights must be [{tokens.T}, {tokens.k}], got {list(weights.shape)}")
-    return weights.contiguous()
+    return weights if weights.is_contiguous() else weights.contiguous()
 
 
 def combine_tokens(rows, tokens: SortedTokens, weights=None, out=None, stream=None):
@@ -326,23 +356,24 @@ def combine_tokens(rows, tokens: SortedTokens, weights=None, out=None, stream=No
     if _elsewhere(device, stream):
         with _on(device, stream):
             return combine_tokens(rows, tokens, weights, out)
-    rows = _readable("rows", rows)
-    H = rows.shape[1]
-    ld_rows = _matrix("rows", rows, tokens.T * tokens.k, H, device)
+    rows, n, H, ld_rows = _readable("rows", rows)
+    if n != tokens.T * tokens.k:
+        raise ValueError(f"rows must be [{tokens.T * tokens.k}, H], got {list(rows.shape)}")
     code = _code("rows", rows)
-    _cuda("tokens.offsets", tokens.offsets, device)
+    if tokens.offsets.device != device:
+        raise ValueError(f"tokens on {tokens.offsets.device}, expected {device}")
     if weights is not None:
         weights = _weights(weights, tokens, device)
     if out is None:
-        out = torch.empty(tokens.T, H, dtype=rows.dtype, device=device)
+        out = torch.empty((tokens.T, H), dtype=rows.dtype, device=device)
         ldy = H
     else:
         ldy = _matrix("out", out, tokens.T, H, device)
         if out.dtype != rows.dtype:
             raise TypeError(f"out is {out.dtype}, rows is {rows.dtype}")
-    check(_abi.sharq_combine_tokens(rows.data_ptr(), ld_rows, H, code, ctypes.byref(tokens.c()),
+    check(_combine_tokens(rows.data_ptr(), ld_rows, H, code, byref(tokens.c()),
                                     None if weights is None else weights.data_ptr(),
-                                    out.data_ptr(), ldy, _stream(None, device)))
+                                    out.data_ptr(), ldy, _current_stream(device.index)))
     return out
 
 
@@ -357,29 +388,31 @@ def combine_tokens_backward(dY, rows, tokens: SortedTokens, weights, d_rows=None
         with _on(device, stream):
             return combine_tokens_backward(dY, rows, tokens, weights, d_rows, d_weights)
     T, k = tokens.T, tokens.k
-    dY, rows = _readable("dY", dY), _readable("rows", rows)
-    H = dY.shape[1]
-    ld_dy = _matrix("dY", dY, T, H, device)
-    ld_rows = _matrix("rows", rows, T * k, H, device)
+    dY, n, H, ld_dy = _readable("dY", dY)
+    _cuda("rows", rows, device)
+    rows, m, h, ld_rows = _readable("rows", rows)
+    if n != T or m != T * k or h != H:
+        raise ValueError(f"dY must be [{T}, H] and rows [{T * k}, H], got {list(dY.shape)} and {list(rows.shape)}")
     code = _code("rows", rows)
     if dY.dtype != rows.dtype:
         raise TypeError(f"dY is {dY.dtype}, rows is {rows.dtype}")
-    _cuda("tokens.offsets", tokens.offsets, device)
+    if tokens.offsets.device != device:
+        raise ValueError(f"tokens on {tokens.offsets.device}, expected {device}")
     weights = _weights(weights, tokens, device)
     if d_rows is None:
-        d_rows = torch.empty(T * k, H, dtype=rows.dtype, device=device)
+        d_rows = torch.empty((T * k, H), dtype=rows.dtype, device=device)
         ld_d = H
     else:
         ld_d = _matrix("d_rows", d_rows, T * k, H, device)
         if d_rows.dtype != rows.dtype:
             raise TypeError(f"d_rows is {d_rows.dtype}, rows is {rows.dtype}")
     if d_weights is None:
-        d_weights = torch.empty(T, k, dtype=torch.float32, device=device)
+        d_weights = torch.empty((T, k), dtype=torch.float32, device=device)
     elif d_weights.dtype != torch.float32 or list(d_weights.shape) != [T, k] or not d_weights.is_contiguous():
         raise ValueError(f"d_weights must be contiguous float32 [{T}, {k}]")
     else:
         _cuda("d_weights", d_weights, device)
-    check(_abi.sharq_combine_tokens_backward(
-        dY.data_ptr(), ld_dy, rows.data_ptr(), ld_rows, H, code, ctypes.byref(tokens.c()),
-        weights.data_ptr(), d_rows.data_ptr(), ld_d, d_weights.data_ptr(), _stream(None, device)))
+    check(_combine_tokens_backward(
+        dY.data_ptr(), ld_dy, rows.data_ptr(), ld_rows, H, code, byref(tokens.c()),
+        weights.data_ptr(), d_rows.data_ptr(), ld_d, d_weights.data_ptr(), _current_stream(device.index)))
     return d_rows, d_weights
