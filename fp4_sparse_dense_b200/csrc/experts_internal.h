@@ -46,8 +46,6 @@ struct SortParams {
   int32_t* order;
   int32_t* place;
 };
-cudaError_t launch_sort(const SortParams& p, unsigned long long ctx, cudaStream_t st);
-
 // Rows moved between token order and expert order. H elements of `dtype` per row; every
 // matrix has a row pitch in elements.
 struct RowsParams {
@@ -62,6 +60,9 @@ struct RowsParams {
   int T, k, H;
 };
 enum RowsOp { kGather = 0, kCombine = 1, kCombineGrad = 2 };
+// Sorts, and gathers rows.tokens_in into rows.rows_out where it is not null.
+cudaError_t launch_sort(const SortParams& p, const RowsParams& rows, int dtype,
+                        unsigned long long ctx, cudaStream_t st);
 cudaError_t launch_rows(const RowsParams& p, RowsOp op, int dtype, cudaStream_t st);
 
 // Allows `kern` up to `smem` bytes of dynamic shared memory in context `ctx`; `done` is the

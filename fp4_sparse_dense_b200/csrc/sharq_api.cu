@@ -836,10 +836,9 @@ sharq_status sharq_sort_tokens(const void* experts, int32_t id_bits, const sharq
   p.offsets = t->offsets;
   p.order = t->order;
   p.place = t->place;
-  s = from_cuda(launch_sort(p, d.ctx_id, st));
+  s = from_cuda(launch_sort(p, r, move ? dtype : SHARQ_BF16, d.ctx_id, st));
   note_launch(d, st, s == SHARQ_OK);
-  if (s != SHARQ_OK || !move) return s;
-  return from_cuda(launch_rows(r, kGather, dtype, st));
+  return s;
 }
 
 sharq_status sharq_sort_tokens_backward(const void* d_rows, size_t ld_d_rows, int32_t H,
