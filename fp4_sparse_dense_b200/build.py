@@ -15,9 +15,9 @@ CSRC = os.path.join(PKG, "csrc")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libsharq.so")
 SOURCES = ["sharq_api.cu", "prep.cu", "quant_weight.cu", "gemm.cu", "gemm_pair.cu",
-           "noalloc.cu", "matvec.cu", "tokens.cu"]
+           "noalloc.cu", "matvec.cu", "matvec_tile.cu", "tokens.cu"]
 HEADERS = ["fp4_device.cuh", "fp4_quant.cuh", "sm100_ptx.cuh", "sharq_internal.h",
-           "epilogue.cuh", "experts_internal.h"]
+           "epilogue.cuh", "experts_internal.h", "matvec_device.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

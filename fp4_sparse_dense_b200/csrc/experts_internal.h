@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "sharq.h"
@@ -32,11 +33,20 @@ struct MatvecParams {
   int splits;  // CTAs of a cluster along K (set by launch_matvec)
   int x_rows;     // rows of activations that stay in shared memory (set by launch_matvec)
   int out_units;  // units whose sums a CTA of a cluster holds (set by launch_matvec)
+  unsigned* status;              // the stream's status word (bounded waits)
+  unsigned long long timeout_ns;
   size_t codes_stride, scales_stride;  // bytes from one expert's weight to the next
 };
 
 cudaError_t launch_matvec(const MatvecParams& p, bool bf16, ScaleView view, int num_sms,
                           unsigned long long ctx, cudaStream_t st);
+
+// The same for more rows, on the tensor cores; `map`: the codes as bytes [E N][K / 2], boxes of
+// 64 x 128 with the 64-byte swizzle.
+cudaError_t launch_matvec_tiles(const CUtensorMap& map, MatvecParams p, bool bf16, ScaleView view,
+                                int num_sms, unsigned long long ctx, cudaStream_t st);
+// Which of the two takes a call.
+inline bool matvec_by_tiles(int M, int E) { return E > 0 ? M > 4 * E : M > 8; }
 
 struct SortParams {
   const void* experts;  // [T * k] int32 or int64

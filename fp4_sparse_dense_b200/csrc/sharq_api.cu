@@ -465,6 +465,23 @@ sharq_status matvec_weight(const void* X, size_t ldx, sharq_dtype dtype, void* c
   return SHARQ_OK;
 }
 
+sharq_status run_matvec(MatvecParams* p, bool bf16, ScaleView view, const DeviceInfo& d,
+                        cudaStream_t st) {
+  CUtensorMap map;
+  const bool tiles = matvec_by_tiles(p->M, p->E);
+  if (tiles) {
+    const sharq_status s = make_map(&map, p->codes, uint64_t(p->K) / 2,
+                                    uint64_t(p->N) * uint64_t(p->E > 0 ? p->E : 1), 64, 128,
+                                    CU_TENSOR_MAP_SWIZZLE_64B);
+    if (s != SHARQ_OK) return s;
+    p->status = status_word(d, st);
+    p->timeout_ns = kWaitLimitNs;
+  }
+  p->early = note_launch(d, st, true) ? 1 : 0;
+  return from_cuda(tiles ? launch_matvec_tiles(map, *p, bf16, view, d.num_sms, d.ctx_id, st)
+                         : launch_matvec(*p, bf16, view, d.num_sms, d.ctx_id, st));
+}
+
 sharq_status check_tokens(const sharq_tokens* t) {
   if (!t || t->T < 0 || t->k < 1 || t->E < 1 || !t->offsets) return SHARQ_ERR_INVALID_ARG;
   if (t->E > 1024 || size_t(t->T) * size_t(t->k) >= (size_t(1) << 30)) return SHARQ_ERR_UNSUPPORTED;
@@ -777,8 +794,7 @@ sharq_status sharq_matvec(const void* X, size_t ldx, int32_t M, sharq_dtype dtyp
   DeviceInfo d;
   if ((s = device_info(&d)) != SHARQ_OK || M == 0) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  p.early = note_launch(d, st, true) ? 1 : 0;
-  return from_cuda(launch_matvec(p, dtype == SHARQ_BF16, view, d.num_sms, d.ctx_id, st));
+  return run_matvec(&p, dtype == SHARQ_BF16, view, d, st);
 }
 
 sharq_status sharq_expert_matvec(const void* X, size_t ldx, int32_t gather, sharq_dtype dtype,
@@ -802,9 +818,7 @@ sharq_status sharq_expert_matvec(const void* X, size_t ldx, int32_t gather, shar
   DeviceInfo d;
   if ((s = device_info(&d)) != SHARQ_OK || p.M == 0) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  s = from_cuda(launch_matvec(p, dtype == SHARQ_BF16, view, d.num_sms, d.ctx_id, st));
-  note_launch(d, st, s == SHARQ_OK);
-  return s;
+  return run_matvec(&p, dtype == SHARQ_BF16, view, d, st);
 }
 
 sharq_status sharq_sort_tokens(const void* experts, int32_t id_bits, const sharq_tokens* t,
