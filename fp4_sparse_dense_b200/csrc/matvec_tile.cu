@@ -15,9 +15,14 @@
 // Operands, all exact: E4M3 * E2M1 as f16 for fp16 activations; bf16 otherwise (E4M3 * E2M1
 // carries 2^-8 until the end; E8M0 * E2M1 as it is). fp16 activations beside E8M0 scales, which
 // may leave f16's range, enter as two bf16 (8 + 3 bits), each in an MMA of its own.
-// Steps rotate over kAccs accumulators, which float32 additions join at the end, so that the
-// accumulator's cut-off bits do not add up over all of K. Where there are too few tiles, the
-// CTAs of a cluster split K and add their sums through distributed shared memory.
+// The tensor core cuts an accumulator's bits below the 24th at every addition, so an accumulator
+// lives for two steps (16 MMAs) of one half of the widening warps: before those warps fill the
+// next operand, which they may only do when the MMAs of the last one have completed, they add
+// it to float32 sums, rounding to nearest. The sums stay in tensor memory as well.
+//
+// CTAs are persistent, two per SM, and every role runs on from tile to tile. Where there are
+// too few tiles, the CTAs of a cluster split K instead, one tile per cluster, and add their sums
+// through distributed shared memory.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -36,17 +41,17 @@ constexpr int kWidenWarps = 8;
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kLoadWarp = 10, kLoadThreads = 128;
 constexpr int kTileThreads = (kLoadWarp + kLoadThreads / 32) * 32;
 constexpr int kWRing = 6;
+constexpr int kGroup = 2;  // steps of a half that share an accumulator
 
 template <int NC, int OPS, int VIEW>
 struct Tile {
-  static constexpr int kAccs = NC == 64 ? 2 : 4;
   static constexpr int kXTile = NC * 256;  // activations of a step: two swizzle atoms of 64 K
   static constexpr int kXStage = OPS == kF16AsTwoBF16 ? 2 * kXTile : kXTile;
-  static constexpr int kXRing = kXStage >= 16384 ? 3 : 4;
+  static constexpr int kXRing = kXStage >= 16384 ? 2 : 4;
   static constexpr int kWStage = 8192 + 1024;  // codes, scales (512 or 1024), 1 KB aligned
   static constexpr int kSmem = kXRing * kXStage + kWRing * kWStage + 1024;
-  // tensor memory: accumulators, then the two operand buffers of 64 columns
-  static constexpr int kColA = kAccs * NC;
+  // tensor memory: two accumulators, two sums, two operand buffers of 64 columns
+  static constexpr int kColSum = 2 * NC, kColA = 4 * NC;
   static constexpr int kCols = 256;
   static_assert(kColA + 128 <= kCols, "tensor memory");
 };
@@ -77,6 +82,17 @@ __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t* r) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // 32 codes of one output (16 bytes) -> sixteen operand words, scaled
@@ -141,20 +157,22 @@ template <int NC, int OPS, int VIEW>
 __global__ void __launch_bounds__(kTileThreads, 2)
 tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
   typedef Tile<NC, OPS, VIEW> C;
+  constexpr int XR = C::kXRing;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const s_x = smem;
-  uint8_t* const s_w = smem + C::kXRing * C::kXStage;
-  __shared__ uint64_t w_full[kWRing], w_empty[kWRing], x_full[C::kXRing], x_empty[C::kXRing];
-  __shared__ uint64_t a_full[2], a_empty[2], acc_full;
+  uint8_t* const s_w = smem + XR * C::kXStage;
+  int* const s_table = reinterpret_cast<int*>(s_w + kWRing * C::kWStage);  // [E + 1] slots before each expert
+  __shared__ uint64_t w_full[kWRing], w_empty[kWRing], x_full[XR], x_empty[XR];
+  __shared__ uint64_t a_full[2], a_empty[2], widen_bar;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ int s_slot[3];  // expert, first row, rows
   volatile int* const abort_flag = &s_abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = p.splits, rank = int(blockIdx.x) % S, nb = int(blockIdx.x) / S;
+  const int S = p.splits, nbs = p.N / 128;
   const int all_steps = p.K / kStepK;
+  const int rank = S > 1 ? int(blockIdx.x) % S : 0;
   const int s_begin = all_steps * rank / S, steps = all_steps * (rank + 1) / S - s_begin;
   const uint64_t limit = p.timeout_ns;
   auto bar = [](const uint64_t* b) { return ptx::smem_u32(b); };
@@ -164,7 +182,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
       ptx::mbar_init(bar(w_full + i), 1);
       ptx::mbar_init(bar(w_empty + i), kWidenWarps / 2);
     }
-    for (int i = 0; i < C::kXRing; ++i) {
+    for (int i = 0; i < XR; ++i) {
       ptx::mbar_init(bar(x_full + i), kLoadThreads);
       ptx::mbar_init(bar(x_empty + i), 1);
     }
@@ -172,7 +190,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
       ptx::mbar_init(bar(a_full + i), kWidenWarps / 2);
       ptx::mbar_init(bar(a_empty + i), 1);
     }
-    ptx::mbar_init(bar(&acc_full), 1);
+    ptx::mbar_init(bar(&widen_bar), kWidenWarps);
     s_abort = 0;
     ptx::fence_mbar_init();
   }
@@ -181,133 +199,212 @@ tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
     ptx::tmem_relinquish();
   }
   if (warp == kCopyWarp && lane == 0) ptx::prefetch_tensormap(&map);
-
-  int e = 0, row0 = int(blockIdx.y) * NC, rows = p.M - row0;
-  bool idle = false;
   if (p.E > 0) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (warp == 0) {
-      // blockIdx.y counts slots of NC rows over all experts
-      int before = 0, found = -1, first = 0, count = 0;
-      for (int base = 0; base < p.E && found < 0; base += 32) {
-        const int ee = base + lane;
-        const int lo = ee < p.E ? p.offsets[ee] : 0, hi = ee < p.E ? p.offsets[ee + 1] : 0;
-        const int chunks = (hi - lo + NC - 1) / NC;
-        int incl = chunks;
+      int before = 0;
+      for (int base = 0; base < p.E; base += 32) {
+        const int e = base + lane;
+        const int rows = e < p.E ? p.offsets[e + 1] - p.offsets[e] : 0;
+        int incl = (rows + NC - 1) / NC;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
           if (lane >= d) incl += v;
         }
-        const int start = before + incl - chunks;
-        const bool mine = int(blockIdx.y) >= start && int(blockIdx.y) < start + chunks;
-        const unsigned who = __ballot_sync(0xFFFFFFFFu, mine);
-        if (who) {
-          const int src = __ffs(who) - 1;
-          found = base + src;
-          const int c = int(blockIdx.y) - start;
-          first = __shfl_sync(0xFFFFFFFFu, lo + c * NC, src);
-          count = __shfl_sync(0xFFFFFFFFu, hi - lo - c * NC, src);
-        }
+        if (e < p.E) s_table[e + 1] = before + incl;
         before += __shfl_sync(0xFFFFFFFFu, incl, 31);
       }
-      if (lane == 0) {
-        s_slot[0] = found;
-        s_slot[1] = first;
-        s_slot[2] = count;
-      }
+      if (lane == 0) s_table[0] = 0;
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tbase = s_tmem;
-  if (p.E > 0) {
-    idle = s_slot[0] < 0;  // the same for every CTA of the cluster
-    e = idle ? 0 : s_slot[0];
-    row0 = s_slot[1];
-    rows = s_slot[2];
-  }
-  rows = idle ? 0 : min(min(rows, NC), p.M - row0);
-  const int n = idle ? 0 : steps;
+
+  // the CTA's tiles: first, first + stride, ... below end (slot-major)
+  const int slots = p.E > 0 ? s_table[p.E] : (p.M + NC - 1) / NC;
+  const int first = S > 1 ? (int(blockIdx.y) < slots ? int(blockIdx.y) * nbs + int(blockIdx.x) / S : 0)
+                          : int(blockIdx.x);
+  const int end = S > 1 ? (int(blockIdx.y) < slots ? first + 1 : 0) : slots * nbs;
+  const int stride = S > 1 ? 1 : int(gridDim.x);
+  const int total = first < end ? (end - first + stride - 1) / stride * steps : 0;
+  auto expert_of = [&](int slot) {
+    if (p.E == 0) return 0;
+    int lo = 0, hi = p.E;  // the last e with table[e] <= slot
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_table[mid] <= slot) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+  auto rows_of = [&](int slot, int e, int* row0) {
+    const int lo = p.E > 0 ? p.offsets[e] : 0, hi = p.E > 0 ? p.offsets[e + 1] : p.M;
+    *row0 = lo + (slot - (p.E > 0 ? s_table[e] : 0)) * NC;
+    return min(min(hi, p.M) - *row0, NC);
+  };
 
   bool ok = true;
-  auto copy_w = [&](int i) {  // one thread
-    const int st = i % kWRing;
+  // the weight of one step after another (one thread)
+  int c_tile = first, c_step = 0, c_y = 0;
+  const uint8_t* c_scales = nullptr;
+  auto copy_w = [&](int g) {
+    if (c_step == 0) {
+      const int slot = c_tile / nbs, nb = c_tile - slot * nbs, e = expert_of(slot);
+      c_y = e * p.N + nb * 128;
+      c_scales = p.scales + size_t(e) * p.scales_stride + (size_t(nb) * all_steps + s_begin) * kScaleStep<VIEW>;
+    }
+    const int st = g % kWRing;
     const uint32_t to = ptx::smem_u32(s_w + st * C::kWStage), fb = bar(w_full + st);
     ptx::mbar_arrive_expect_tx(fb, 8192 + kScaleStep<VIEW>);
-    ptx::tma_load_2d(to, &map, (s_begin + i) * 64, e * p.N + nb * 128, fb);
-    ptx::bulk_load(to + 8192,
-                   p.scales + size_t(e) * p.scales_stride +
-                       (size_t(nb) * all_steps + s_begin + i) * kScaleStep<VIEW>,
-                   kScaleStep<VIEW>, fb);
+    ptx::tma_load_2d(to, &map, (s_begin + c_step) * 64, c_y, fb);
+    ptx::bulk_load(to + 8192, c_scales + size_t(c_step) * kScaleStep<VIEW>, kScaleStep<VIEW>, fb);
+    if (++c_step == steps) {
+      c_step = 0;
+      c_tile += stride;
+    }
   };
   int early = 0;  // steps whose weight was asked for before the kernels before had completed
   if (p.E == 0) {
     if (p.early && warp == kCopyWarp) {
-      early = min(n, kWRing);
+      early = min(total, kWRing);
       if (lane == 0)
-        for (int i = 0; i < early; ++i) copy_w(i);
+        for (int g = 0; g < early; ++g) copy_w(g);
     }
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
   }
+  // the same answer in the whole warp
+  auto wait_warp = [&](const uint64_t* b, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, ptx::mbar_wait(bar(b), parity, abort_flag, limit)) != 0;
+  };
 
   if (warp < kWidenWarps) {
     // ------------------------------------------------------------------ widening
     const int set = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t ta = tbase + (uint32_t(quarter * 32) << 16) + C::kColA + set * 64;
-    auto wait = [&](const uint64_t* b, uint32_t parity) {  // the same answer in the whole warp
-      return __all_sync(0xFFFFFFFFu, ptx::mbar_wait(bar(b), parity, abort_flag, limit)) != 0;
-    };
-    for (int i = set; i < n; i += 2) {
-      const int st = i % kWRing;
-      if (!wait(w_full + st, (i / kWRing) & 1)) { ok = false; break; }
-      const uint8_t* w = s_w + st * C::kWStage;
-      uint4 c[4];
+    const uint32_t t_acc = tbase + (uint32_t(quarter * 32) << 16) + set * NC;
+    const uint32_t t_sum = tbase + (uint32_t(quarter * 32) << 16) + C::kColSum;
+    // adds the half's accumulator to its sums
+    auto fold = [&](bool fresh) {
+#pragma unroll 1
+      for (int m0 = 0; m0 < NC; m0 += 8) {
+        uint32_t v[8], t[8];
+        tmem_ld_8(t_acc + m0, v);
+        if (!fresh) tmem_ld_8(t_sum + set * NC + m0, t);
+        ptx::tmem_ld_wait();
+        if (!fresh) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)  // TMA's 64-byte swizzle: unit ^ (row / 2) % 4
-        c[j] = *reinterpret_cast<const uint4*>(w + row * 64 + ((j ^ ((row >> 1) & 3)) * 16));
-      const uint32_t sc0 = *reinterpret_cast<const uint32_t*>(w + 8192 + lane * 16 + quarter * 4);
-      const uint32_t sc1 =
-          VIEW == kE4M3x16 ? *reinterpret_cast<const uint32_t*>(w + 8192 + 512 + lane * 16 + quarter * 4) : 0u;
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(w_empty + st));
-      if (i >= 2 && !wait(a_empty + set, ((i >> 1) - 1) & 1)) { ok = false; break; }
-      ptx::tc_fence_after();
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t f0, f1, a[16];
-        if (VIEW == kE4M3x16) {
-          const uint32_t s = j < 2 ? sc0 : sc1;
-          f0 = scale_factor<OPS, VIEW>((s >> ((j & 1) * 16)) & 0xFFu);
-          f1 = scale_factor<OPS, VIEW>((s >> ((j & 1) * 16 + 8)) & 0xFFu);
-        } else {
-          f0 = f1 = scale_factor<OPS, VIEW>((sc0 >> (j * 8)) & 0xFFu);
+          for (int i = 0; i < 8; ++i)
+            v[i] = __float_as_uint(__uint_as_float(t[i]) + __uint_as_float(v[i]));
         }
-        widen_block<OPS, VIEW>(c[j], f0, f1, a);
-        tmem_st_16(ta + j * 16, a);
+        tmem_st_8(t_sum + set * NC + m0, v);
       }
       tmem_st_wait();
+    };
+    // all widening warps meet; a timeout ends the wait
+    int met = 0;
+    auto meet = [&]() {
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(a_full + set));
+      if (lane == 0) ptx::mbar_arrive(bar(&widen_bar));
+      const bool done = wait_warp(&widen_bar, met++ & 1);
+      ptx::tc_fence_after();
+      return done;
+    };
+    for (int tile = first, g0 = 0; tile < end && ok; tile += stride, g0 += steps) {
+      int own = 0;  // steps of this half in the tile
+      for (int g = g0 + ((g0 ^ set) & 1); g < g0 + steps; g += 2, ++own) {
+        const int st = g % kWRing;
+        if (!wait_warp(w_full + st, (g / kWRing) & 1)) { ok = false; break; }
+        const uint8_t* w = s_w + st * C::kWStage;
+        uint4 c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // TMA's 64-byte swizzle: unit ^ (row / 2) % 4
+          c[j] = *reinterpret_cast<const uint4*>(w + row * 64 + ((j ^ ((row >> 1) & 3)) * 16));
+        const uint32_t sc0 = *reinterpret_cast<const uint32_t*>(w + 8192 + lane * 16 + quarter * 4);
+        const uint32_t sc1 =
+            VIEW == kE4M3x16 ? *reinterpret_cast<const uint32_t*>(w + 8192 + 512 + lane * 16 + quarter * 4) : 0u;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(w_empty + st));
+        if (g >= 2 && !wait_warp(a_empty + set, ((g >> 1) - 1) & 1)) { ok = false; break; }
+        ptx::tc_fence_after();
+        if (own > 0 && own % kGroup == 0) fold(own == kGroup);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t f0, f1, a[16];
+          if (VIEW == kE4M3x16) {
+            const uint32_t s = j < 2 ? sc0 : sc1;
+            f0 = scale_factor<OPS, VIEW>((s >> ((j & 1) * 16)) & 0xFFu);
+            f1 = scale_factor<OPS, VIEW>((s >> ((j & 1) * 16 + 8)) & 0xFFu);
+          } else {
+            f0 = f1 = scale_factor<OPS, VIEW>((sc0 >> (j * 8)) & 0xFFu);
+          }
+          widen_block<OPS, VIEW>(c[j], f0, f1, a);
+          tmem_st_16(ta + j * 16, a);
+        }
+        tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(a_full + set));
+      }
+      if (!ok) break;
+      // the tile's outputs: both halves' sums (a tile has two steps at least), 16 rows at a time
+      // by turns. g1: the half's last step.
+      const int g1 = g0 + steps - 1 - ((g0 + steps - 1 - set) & 1);
+      if (!wait_warp(a_empty + set, (g1 >> 1) & 1)) { ok = false; break; }
+      ptx::tc_fence_after();
+      fold(own <= kGroup);
+      if (!meet()) { ok = false; break; }
+      const int slot = tile / nbs, nb = tile - slot * nbs, e = expert_of(slot);
+      int row0;
+      const int rows = rows_of(slot, e, &row0);
+      const float scale = p.w_scale[size_t(e) * 4] * (OPS != kF16Operands && VIEW != kE8M0x32 ? 256.f : 1.f);
+      const size_t at = size_t(row0) * p.ldy + nb * 128 + row;
+#pragma unroll 1
+      for (int m0 = set * 16; m0 < rows; m0 += 32) {
+        uint32_t v[16], t[16];
+        tmem_ld_16(t_sum + m0, v);
+        tmem_ld_16(t_sum + NC + m0, t);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(t[i]));
+        if (S > 1) {
+          float* const s_part = reinterpret_cast<float*>(smem);  // [row][128]: all steps are done
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s_part[(m0 + i) * 128 + row] = __uint_as_float(v[i]);
+          continue;
+        }
+        auto store = [&](auto* y, auto make) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (m0 + i < rows) y[at + size_t(m0 + i) * p.ldy] = make(__uint_as_float(v[i]) * scale);
+        };
+        if (p.y_dtype == SHARQ_F32)
+          store(static_cast<float*>(p.Y), [](float f) { return f; });
+        else if (p.y_dtype == SHARQ_BF16)
+          store(static_cast<__nv_bfloat16*>(p.Y), [](float f) { return __float2bfloat16_rn(f); });
+        else
+          store(static_cast<__half*>(p.Y), [](float f) { return __float2half_rn(f); });
+      }
+      if (!meet()) { ok = false; break; }  // both have read the sums
     }
   } else if (warp == kCopyWarp) {
     // ------------------------------------------------------------------ the weight's copies
     if (lane == 0) {
-      int i = early;
-      for (; i < n; ++i) {
-        if (i >= kWRing &&
-            !ptx::mbar_wait(bar(w_empty + i % kWRing), (i / kWRing - 1) & 1, abort_flag, limit)) {
+      int g = early;
+      for (; g < total; ++g) {
+        if (g >= kWRing &&
+            !ptx::mbar_wait(bar(w_empty + g % kWRing), (g / kWRing - 1) & 1, abort_flag, limit)) {
           ok = false;
           break;
         }
-        copy_w(i);
+        copy_w(g);
       }
       if (!ok)  // copies in flight land before the CTA leaves
-        for (int k = i > kWRing ? i - kWRing : 0; k < i; ++k) {
+        for (int k = g > kWRing ? g - kWRing : 0; k < g; ++k) {
           const uint64_t t0 = ptx::globaltimer();
           while (!ptx::mbar_try_wait(bar(w_full + k % kWRing), (k / kWRing) & 1) && ptx::globaltimer() - t0 < limit) {}
         }
@@ -317,81 +414,97 @@ tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
     if (ptx::elect_one()) {
       const uint32_t type = OPS == kF16Operands ? 0u : (1u << 7) | (1u << 10);
       const uint32_t idesc = (1u << 4) | type | (uint32_t(NC >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-      for (int i = 0; i < n; ++i) {
-        const int st = i % C::kXRing;
-        if (!ptx::mbar_wait(bar(x_full + st), (i / C::kXRing) & 1, abort_flag, limit) ||
-            !ptx::mbar_wait(bar(a_full + (i & 1)), (i >> 1) & 1, abort_flag, limit)) {
+      // an operand's descriptor is the first stage's plus its offset in 16-byte units, which never
+      // leaves the address field
+      const uint64_t desc = ptx::smem_desc(ptx::smem_u32(s_x), 16, 1024, 2);
+      int own[2] = {0, 0};  // steps of each half in the tile
+      for (int g = 0, i = 0; g < total; ++g) {
+        const int st = g % XR, half = g & 1;
+        if (!ptx::mbar_wait(bar(x_full + st), (g / XR) & 1, abort_flag, limit) ||
+            !ptx::mbar_wait(bar(a_full + half), (g >> 1) & 1, abort_flag, limit)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t d = tbase + (i % C::kAccs) * NC, a = tbase + C::kColA + (i & 1) * 64;
-        const uint32_t x = ptx::smem_u32(s_x + st * C::kXStage);
-        uint32_t acc = i >= C::kAccs ? 1u : 0u;
+        const uint32_t d = tbase + half * NC, a = tbase + C::kColA + half * 64;
+        const uint64_t x = desc + uint32_t(st * (C::kXStage >> 4));
+        uint32_t acc = (half ? own[1] : own[0]) % kGroup != 0 ? 1u : 0u;
 #pragma unroll
         for (int t = 0; t < (OPS == kF16AsTwoBF16 ? 2 : 1); ++t)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            mma_ts(d, a + j * 8,
-                   ptx::smem_desc(x + t * C::kXTile + (j >> 2) * (NC * 128) + (j & 3) * 32, 16, 1024, 2),
+            mma_ts(d, a + j * 8, x + uint32_t((t * C::kXTile + (j >> 2) * (NC * 128) + (j & 3) * 32) >> 4),
                    idesc, acc);
             acc = 1u;
           }
-        ptx::mma_commit(bar(a_empty + (i & 1)));
+        ptx::mma_commit(bar(a_empty + half));
         ptx::mma_commit(bar(x_empty + st));
+        if (half) ++own[1]; else ++own[0];
+        if (++i == steps) i = own[0] = own[1] = 0;
       }
-      if (n > 0) {  // every MMA issued above has completed once this arrives
-        ptx::mma_commit(bar(&acc_full));
-        if (!ptx::mbar_wait(bar(&acc_full), 0, abort_flag, limit)) ok = false;
-      }
+      // every MMA issued above has completed before the CTA leaves
+      for (int g = total > 2 ? total - 2 : 0; g < total && ok; ++g)
+        if (!ptx::mbar_wait(bar(a_empty + (g & 1)), (g >> 1) & 1, abort_flag, limit)) ok = false;
     }
   } else {
     // ------------------------------------------------------------------ the activations
     const int tid = threadIdx.x - kLoadWarp * 32, r8 = tid >> 4, c = tid & 15;
     const uint16_t* src[NC / 8];
-#pragma unroll
-    for (int m = 0; m < NC / 8; ++m) {
-      const int r = m * 8 + r8;
-      src[m] = nullptr;
-      if (r < rows)
-        src[m] = static_cast<const uint16_t*>(p.X) +
-                 size_t(p.order ? p.order[row0 + r] / p.k : row0 + r) * p.ldx + size_t(s_begin) * kStepK + c * 8;
-    }
     // 16-byte unit c of row r: atom c / 8 (64 K), unit (c % 8) ^ (r % 8)
-    const uint32_t to = ptx::smem_u32(s_x) + (c >> 3) * (NC * 128) + r8 * 128 + (((c & 7) ^ r8) << 4);
-    constexpr int kAhead = C::kXRing - 1;
-    for (int i = 0; i < n + kAhead; ++i) {
-      if (i < n) {
-        const int st = i % C::kXRing;
-        if (i >= C::kXRing &&
-            !ptx::mbar_wait(bar(x_empty + st), (i / C::kXRing - 1) & 1, abort_flag, limit)) {
+    const uint32_t to = (c >> 3) * (NC * 128) + r8 * 128 + (((c & 7) ^ r8) << 4);
+    constexpr int kAhead = XR - 1;
+    int x_tile = first, x_step = 0;  // next step to copy
+    for (int g = 0; g < total + kAhead; ++g) {
+      if (g < total) {
+        const int st = g % XR;
+        if (x_step == 0) {
+          const int slot = x_tile / nbs, e = expert_of(slot);
+          int row0;
+          const int rows = rows_of(slot, e, &row0);
+#pragma unroll
+          for (int m = 0; m < NC / 8; ++m) {
+            const int r = m * 8 + r8;
+            src[m] = nullptr;
+            if (r < rows)
+              src[m] = static_cast<const uint16_t*>(p.X) +
+                       size_t(p.order ? p.order[row0 + r] / p.k : row0 + r) * p.ldx +
+                       size_t(s_begin) * kStepK + c * 8;
+          }
+        }
+        if (g >= XR && !ptx::mbar_wait(bar(x_empty + st), (g / XR - 1) & 1, abort_flag, limit)) {
           ok = false;
           break;
         }
 #pragma unroll
         for (int m = 0; m < NC / 8; ++m)
-          if (src[m]) copy_async<16>(to + st * C::kXStage + m * 1024, src[m] + size_t(i) * kStepK);
+          if (src[m]) {
+            copy_async<16>(ptx::smem_u32(s_x + st * C::kXStage) + to + m * 1024, src[m]);
+            src[m] += kStepK;
+          }
+        if (++x_step == steps) {
+          x_step = 0;
+          x_tile += stride;
+        }
       }
       copies_commit();
-      if (i >= kAhead) {
-        const int st = (i - kAhead) % C::kXRing;
+      if (g >= kAhead) {
+        const int st = (g - kAhead) % XR;
         copies_wait<kAhead>();
         if (OPS != kF16Operands) {
 #pragma unroll
-          for (int m = 0; m < NC / 8; ++m)
-            if (src[m]) {
-              uint8_t* at = s_x + (to - ptx::smem_u32(s_x)) + st * C::kXStage + m * 1024;
-              uint4 v = pair_up(*reinterpret_cast<const uint4*>(at));
-              if (OPS == kF16AsTwoBF16) {
-                uint4 lo;
-                split_f16(v.x, &v.x, &lo.x);
-                split_f16(v.y, &v.y, &lo.y);
-                split_f16(v.z, &v.z, &lo.z);
-                split_f16(v.w, &v.w, &lo.w);
-                *reinterpret_cast<uint4*>(at + C::kXTile) = lo;
-              }
-              *reinterpret_cast<uint4*>(at) = v;
+          for (int m = 0; m < NC / 8; ++m) {  // rows that were not copied hold anything
+            uint8_t* at = s_x + st * C::kXStage + to + m * 1024;
+            uint4 v = pair_up(*reinterpret_cast<const uint4*>(at));
+            if (OPS == kF16AsTwoBF16) {
+              uint4 lo;
+              split_f16(v.x, &v.x, &lo.x);
+              split_f16(v.y, &v.y, &lo.y);
+              split_f16(v.z, &v.z, &lo.z);
+              split_f16(v.w, &v.w, &lo.w);
+              *reinterpret_cast<uint4*>(at + C::kXTile) = lo;
             }
+            *reinterpret_cast<uint4*>(at) = v;
+          }
         }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(bar(x_full + st));
@@ -404,63 +517,33 @@ tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
     atomicExch(p.status, unsigned(SHARQ_ERR_TIMEOUT));
   }
 
-  // ------------------------------------------------------------------ epilogue
-  // Warps 0 ... 3: a thread has one output and all rows of the slot.
-  float* const s_part = reinterpret_cast<float*>(smem);  // [row][128], in the activations' place
-  if (warp < 4 && n > 0) {
-    if (ok && !ptx::mbar_wait(bar(&acc_full), 0, abort_flag, limit)) {
-      s_abort = 1;
-      atomicExch(p.status, unsigned(SHARQ_ERR_TIMEOUT));
-    }
-    ptx::tc_fence_after();
-    const uint32_t td = tbase + (uint32_t(warp * 32) << 16);
-    const float scale = p.w_scale[size_t(e) * 4] * (OPS != kF16Operands && VIEW != kE8M0x32 ? 256.f : 1.f);
-    const int r = warp * 32 + lane;
-#pragma unroll 1
-    for (int m0 = 0; m0 < rows; m0 += 16) {
-      uint32_t v[16];
-      float sum[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sum[i] = 0.f;
-      const int accs = min(n, C::kAccs);
-#pragma unroll 1
-      for (int a = 0; a < accs; ++a) {
-        tmem_ld_16(td + a * NC + m0, v);
-        ptx::tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] += __uint_as_float(v[i]);
-      }
-      if (S > 1) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s_part[(m0 + i) * 128 + r] = sum[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (m0 + i < rows) store_y(p, size_t(row0 + m0 + i) * p.ldy + nb * 128 + r, sum[i] * scale);
-      }
-    }
-    ptx::tc_fence_before();
-  }
   if (S > 1) {
     ptx::cluster_sync();
-    const float scale = p.w_scale[size_t(e) * 4] * (OPS != kF16Operands && VIEW != kE8M0x32 ? 256.f : 1.f);
-    const int per = 128 / S, r = rank * per + (int(threadIdx.x) & (per - 1));
-    const int groups = kTileThreads / per;
-    for (int m = int(threadIdx.x) / per; m < rows && int(threadIdx.x) / per < groups; m += groups) {
-      const uint32_t a = ptx::smem_u32(s_part + m * 128 + r);
-      float v[8];
+    if (total > 0) {
+      const int slot = first / nbs, nb = first - slot * nbs, e = expert_of(slot);
+      int row0;
+      const int rows = rows_of(slot, e, &row0);
+      const float scale = p.w_scale[size_t(e) * 4] * (OPS != kF16Operands && VIEW != kE8M0x32 ? 256.f : 1.f);
+      const float* const s_part = reinterpret_cast<const float*>(smem);
+      const int per = 128 / S, r = rank * per + (int(threadIdx.x) & (per - 1));
+      const int groups = kTileThreads / per, group = int(threadIdx.x) / per;
+      for (int m = group; m < rows && group < groups; m += groups) {
+        const uint32_t a = ptx::smem_u32(s_part + m * 128 + r);
+        float v[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        v[c] = 0.f;
-        if (c < S) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[c]) : "r"(ptx::mapa(a, uint32_t(c))));
+        for (int c = 0; c < 8; ++c) {
+          v[c] = 0.f;
+          if (c < S) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[c]) : "r"(ptx::mapa(a, uint32_t(c))));
+        }
+        float sum = v[0];
+#pragma unroll
+        for (int c = 1; c < 8; ++c) sum += v[c];
+        store_y(p, size_t(row0 + m) * p.ldy + nb * 128 + r, sum * scale);
       }
-      float sum = v[0];
-#pragma unroll
-      for (int c = 1; c < 8; ++c) sum += v[c];
-      store_y(p, size_t(row0 + m) * p.ldy + nb * 128 + r, sum * scale);
     }
     ptx::cluster_sync();  // no CTA leaves while its sums are read
   } else {
+    ptx::tc_fence_before();
     __syncthreads();
   }
   if (warp == kMmaWarp) {
@@ -470,17 +553,23 @@ tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
 }
 
 template <int NC, int OPS, int VIEW>
-cudaError_t launch_tile(const CUtensorMap& map, const MatvecParams& p, unsigned slots,
+cudaError_t launch_tile(const CUtensorMap& map, const MatvecParams& p, unsigned slots, int num_sms,
                         unsigned long long ctx, cudaStream_t st) {
   auto* kern = tile_kernel<NC, OPS, VIEW>;
   constexpr int kSmem = Tile<NC, OPS, VIEW>::kSmem;
   static std::atomic<unsigned long long> done{~0ull};
-  const cudaError_t e = allow_smem(kern, kSmem, ctx, &done);
+  const cudaError_t e = allow_smem(kern, kSmem + 1025 * 4, ctx, &done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.N / 128 * p.splits), slots);
+  if (p.splits > 1) {
+    cfg.gridDim = dim3(unsigned(p.N / 128 * p.splits), slots);
+  } else {
+    const unsigned long long tiles = (unsigned long long)(p.N / 128) * slots;
+    const unsigned most = unsigned(num_sms) * 2u;
+    cfg.gridDim = dim3(tiles < most ? unsigned(tiles) : most);
+  }
   cfg.blockDim = dim3(kTileThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = size_t(kSmem + (p.E > 0 ? (p.E + 1) * 4 : 0));
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -496,17 +585,17 @@ cudaError_t launch_tile(const CUtensorMap& map, const MatvecParams& p, unsigned 
 
 template <int NC>
 cudaError_t launch_nc(const CUtensorMap& map, const MatvecParams& p, bool bf16, ScaleView view,
-                      unsigned slots, unsigned long long ctx, cudaStream_t st) {
+                      unsigned slots, int num_sms, unsigned long long ctx, cudaStream_t st) {
   switch (view) {
     case kE4M3x16:
-      return bf16 ? launch_tile<NC, kBF16Operands, kE4M3x16>(map, p, slots, ctx, st)
-                  : launch_tile<NC, kF16Operands, kE4M3x16>(map, p, slots, ctx, st);
+      return bf16 ? launch_tile<NC, kBF16Operands, kE4M3x16>(map, p, slots, num_sms, ctx, st)
+                  : launch_tile<NC, kF16Operands, kE4M3x16>(map, p, slots, num_sms, ctx, st);
     case kE4M3x32:
-      return bf16 ? launch_tile<NC, kBF16Operands, kE4M3x32>(map, p, slots, ctx, st)
-                  : launch_tile<NC, kF16Operands, kE4M3x32>(map, p, slots, ctx, st);
+      return bf16 ? launch_tile<NC, kBF16Operands, kE4M3x32>(map, p, slots, num_sms, ctx, st)
+                  : launch_tile<NC, kF16Operands, kE4M3x32>(map, p, slots, num_sms, ctx, st);
     default:
-      return bf16 ? launch_tile<NC, kBF16Operands, kE8M0x32>(map, p, slots, ctx, st)
-                  : launch_tile<NC, kF16AsTwoBF16, kE8M0x32>(map, p, slots, ctx, st);
+      return bf16 ? launch_tile<NC, kBF16Operands, kE8M0x32>(map, p, slots, num_sms, ctx, st)
+                  : launch_tile<NC, kF16AsTwoBF16, kE8M0x32>(map, p, slots, num_sms, ctx, st);
   }
 }
 
@@ -514,25 +603,36 @@ cudaError_t launch_nc(const CUtensorMap& map, const MatvecParams& p, bool bf16, 
 
 cudaError_t launch_matvec_tiles(const CUtensorMap& map, MatvecParams p, bool bf16, ScaleView view,
                                 int num_sms, unsigned long long ctx, cudaStream_t st) {
-  // Rows per slot: 16, 32 or 64. An expert's rows are not known here, twice their mean stands
-  // for them.
+  // Rows per slot: 16 or 32. An expert's rows are not known here, twice their mean stands for
+  // them.
   const int want = p.E > 0 ? 2 * ((p.M + p.E - 1) / p.E) : p.M;
-  const int nc = want <= 16 ? 16 : want <= 32 ? 32 : 64;
-  unsigned slots = unsigned((p.M + nc - 1) / nc), busy = slots;
+  const int nc = want <= 16 ? 16 : 32;
+  unsigned slots = unsigned((p.M + nc - 1) / nc);
+  double busy = slots;
   if (p.E > 0) {
     // sum over experts of ceil(rows / nc) <= experts with rows + M / nc
-    busy = unsigned(p.E < p.M ? p.E : p.M);
-    slots = busy + unsigned(p.M / nc);
+    const int used = p.E < p.M ? p.E : p.M;
+    slots = unsigned(used + p.M / nc);
+    busy = used + 0.5 * (p.M / nc);
   }
   if (slots > 65535u) return cudaErrorInvalidConfiguration;  // bounded by the caller's checks
-  // K over a cluster of CTAs, as many as run at once (two per SM), four steps each at least
+  // K over a cluster of S CTAs, four steps each at least, where that gives the least time: S == 1
+  // shares whole tiles out over the CTAs that run at once, S > 1 pays a CTA's start and end
+  // (about 6 steps) in every round.
+  const int steps = p.K / kStepK;
+  const double run = num_sms * 2.0, tiles = busy * (p.N / 128);
+  auto rounds = [](double n) { return double((long long)(n + 0.999)); };
+  double best = rounds(tiles / run) * steps + 6.0;
   p.splits = 1;
-  while (p.splits < 8 && p.splits * 2 * 4 <= p.K / kStepK &&
-         unsigned(p.N / 128) * busy * unsigned(p.splits) * 2u <= unsigned(num_sms) * 2u)
-    p.splits *= 2;
-  if (nc == 16) return launch_nc<16>(map, p, bf16, view, slots, ctx, st);
-  if (nc == 32) return launch_nc<32>(map, p, bf16, view, slots, ctx, st);
-  return launch_nc<64>(map, p, bf16, view, slots, ctx, st);
+  for (int S = 2; S <= 8 && S * 4 <= steps; S *= 2) {
+    const double cost = rounds(tiles * S / run) * (double(steps) / S + 6.0);
+    if (cost < best) {
+      best = cost;
+      p.splits = S;
+    }
+  }
+  if (nc == 16) return launch_nc<16>(map, p, bf16, view, slots, num_sms, ctx, st);
+  return launch_nc<32>(map, p, bf16, view, slots, num_sms, ctx, st);
 }
 
 }  // namespace sharq
