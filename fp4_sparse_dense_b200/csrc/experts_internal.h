@@ -30,7 +30,7 @@ struct MatvecParams {
                            // and X holds tokens; null: X holds the sorted rows themselves
   int E, k;
   int early;  // the weight may be loaded before the kernel launched just before has completed
-  int splits;  // CTAs of a cluster along K (set by launch_matvec)
+  int splits;     // CTAs of a cluster along K (set by the launch)
   int x_rows;     // rows of activations that stay in shared memory (set by launch_matvec)
   int out_units;  // units whose sums a CTA of a cluster holds (set by launch_matvec)
   unsigned* status;              // the stream's status word (bounded waits)
@@ -45,8 +45,8 @@ cudaError_t launch_matvec(const MatvecParams& p, bool bf16, ScaleView view, int 
 // 64 x 128 with the 64-byte swizzle.
 cudaError_t launch_matvec_tiles(const CUtensorMap& map, MatvecParams p, bool bf16, ScaleView view,
                                 int num_sms, unsigned long long ctx, cudaStream_t st);
-// Which of the two takes a call.
-inline bool matvec_by_tiles(int M, int E) { return E > 0 ? M > 4 * E : M > 8; }
+// Whether launch_matvec takes a call: few rows, whose activations fit into shared memory.
+bool matvec_streams(int M, int E, int K);
 
 struct SortParams {
   const void* experts;  // [T * k] int32 or int64

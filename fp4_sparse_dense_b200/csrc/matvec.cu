@@ -15,11 +15,12 @@
 // asynchronous copies; the sums of the warps and CTAs that share an output meet in shared
 // memory, in a fixed order.
 //
-// The grid is one CTA per SM. A CTA keeps the activations of its slot (up to 8 MT rows of one
+// The grid is one CTA per SM. A CTA keeps the activations of its slot (up to 8 rows of one
 // weight) in shared memory, read and converted once, and takes an equal run of the list of
 // 32-output units; its warps split the run's steps evenly, whatever unit they belong to, so
 // that there is one prologue and one sum per CTA and slot. Where the activations do not fit, a
-// cluster of S CTAs splits K and its CTAs add their sums through distributed shared memory.
+// cluster of S CTAs splits K, works through the same units and adds its sums through
+// distributed shared memory. More rows go to tile_kernel (matvec_tile.cu).
 //
 // The widening sets the kernel's issue rate, so it uses the conversion instruction (two codes
 // to f16x2) and one packed multiply by the scale. That makes the weight an f16 operand:
@@ -122,24 +123,14 @@ __device__ __forceinline__ uint4 scale_bf16(uint4 v, float* undo, bool* wide) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int MT>
 struct Acc {
-  float v[MT][2][4];  // (h, c): output 32 (2 h + c / 2) + g of the lane's quarter, row 2 t + c % 2
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[m][h][c] = 0.f;
-  }
+  float v[2][4];  // (h, c): output 32 (2 h + c / 2) + g of the lane's quarter, row 2 t + c % 2
 };
 
-// One step with f16 operands. load_x(m, q): the lane's activations of row 8 m + g, K unit
-// 4 t + q of the step; load_undo(m): what takes the scaling of rows 8 m + 2 t and + 1 out.
-template <int MT, int VIEW, bool SCALED, typename LoadX, typename LoadUndo>
-__device__ __forceinline__ void step_f16(Acc<MT>& acc, const Stage& st, int rows, LoadX load_x,
-                                         LoadUndo load_undo) {
+// One step with f16 operands. x: the lane's row at its K unit 4 t of the step, unit 4 t + q 64 q
+// bytes on; undo: what takes the scaling of rows 2 t and 2 t + 1 out.
+template <int VIEW, bool SCALED>
+__device__ __forceinline__ void step_f16(Acc& acc, const Stage& st, const uint8_t* x, const float* undo) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t pick = uint32_t(t) | uint32_t(4 + t) << 4;  // byte t of two words
   const uint4 sv = st.scales[VIEW == kE4M3x16 ? t >> 1 : 0][g];
@@ -201,7 +192,7 @@ __device__ __forceinline__ void step_f16(Acc<MT>& acc, const Stage& st, int rows
         f[i][1] = f[i][0];
       }
     }
-    float part[MT][2][4];
+    float part[2][4];
     const uint4 cw[4] = {st.codes[0][lane], st.codes[1][lane], st.codes[2][lane], st.codes[3][lane]};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -213,45 +204,37 @@ __device__ __forceinline__ void step_f16(Acc<MT>& acc, const Stage& st, int rows
 #pragma unroll
         for (int j = 0; j < 4; ++j) a[i][j] = mul_f16x2(a[i][j], f[i][q >> 1]);
       }
+      const uint4 b = *reinterpret_cast<const uint4*>(x + q * 64);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        if (MT > 1 && m * 8 >= rows) break;
-        const uint4 b = load_x(m, q);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (q == 0)
-            mma_f16_first(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
-          else
-            mma_f16(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
-          mma_f16(part[m][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
-        }
+      for (int h = 0; h < 2; ++h) {
+        if (q == 0)
+          mma_f16_first(part[h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
+        else
+          mma_f16(part[h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
+        mma_f16(part[h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
       }
     }
+    float2 out = make_float2(1.f, 1.f);
+    if (SCALED) out = *reinterpret_cast<const float2*>(undo);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if (MT > 1 && m * 8 >= rows) break;
-      float2 undo = make_float2(1.f, 1.f);
-      if (SCALED) undo = load_undo(m);
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float v = part[m][h][c], x = c & 1 ? undo.y : undo.x;
-          float& to = acc.v[m][h][c];
-          if (VIEW == kE8M0x32)
-            to = fmaf(SCALED ? v * x : v, ref[2 * h + (c >> 1)], to);
-          else
-            to = SCALED ? fmaf(v, x, to) : to + v;
-        }
-    }
+      for (int c = 0; c < 4; ++c) {
+        const float v = part[h][c], o = c & 1 ? out.y : out.x;
+        float& to = acc.v[h][c];
+        if (VIEW == kE8M0x32)
+          to = fmaf(SCALED ? v * o : v, ref[2 * h + (c >> 1)], to);
+        else
+          to = SCALED ? fmaf(v, o, to) : to + v;
+      }
   } while (VIEW == kE8M0x32 && ++wp < wpasses);
 }
 
 // One step with bf16 operands: the widened codes' 2^-126 is taken out by the scale's factor
 // (E4M3: sf * 2^118, finite up to 448; E8M0: 2^(126 + b - b_max)), the rest with the sum.
 // The codes go in step_f16's order, so that both kinds of operands give the same bits.
-template <int MT, int VIEW, typename LoadX>
-__device__ __forceinline__ void step_bf16(Acc<MT>& acc, const Stage& st, int rows, LoadX load_x) {
+template <int VIEW>
+__device__ __forceinline__ void step_bf16(Acc& acc, const Stage& st, const uint8_t* x) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint4 sv = st.scales[VIEW == kE4M3x16 ? t >> 1 : 0][g];
   const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
@@ -278,13 +261,11 @@ __device__ __forceinline__ void step_bf16(Acc<MT>& acc, const Stage& st, int row
       ref[i] = 256.f;
     }
   }
-  float part[MT][2][4];
+  float part[2][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) part[m][h][c] = 0.f;
+    for (int c = 0; c < 4; ++c) part[h][c] = 0.f;
 #pragma unroll 1
   for (int q = 0; q < 4; ++q) {
     uint32_t a[4][4];
@@ -299,42 +280,31 @@ __device__ __forceinline__ void step_bf16(Acc<MT>& acc, const Stage& st, int row
       a[i][2] = __byte_perm(h[0], h[1], 0x7632);
       a[i][3] = __byte_perm(h[2], h[3], 0x7632);
     }
+    const uint4 b = *reinterpret_cast<const uint4*>(x + q * 64);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if (MT > 1 && m * 8 >= rows) break;
-      const uint4 b = load_x(m, q);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mma_bf16(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
-        mma_bf16(part[m][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
-      }
+    for (int h = 0; h < 2; ++h) {
+      mma_bf16(part[h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
+      mma_bf16(part[h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
     }
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (MT > 1 && m * 8 >= rows) break;
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        acc.v[m][h][c] = fmaf(part[m][h][c], ref[2 * h + (c >> 1)], acc.v[m][h][c]);
-  }
+    for (int c = 0; c < 4; ++c) acc.v[h][c] = fmaf(part[h][c], ref[2 * h + (c >> 1)], acc.v[h][c]);
 }
 
 // A lane's sums of a whole unit -> Y, at the lane's first output and row.
-template <int MT, int Y>
-__device__ __forceinline__ void store_unit(const MatvecParams& p, const Acc<MT>& acc, size_t at,
+template <int Y>
+__device__ __forceinline__ void store_unit(const MatvecParams& p, const Acc& acc, size_t at,
                                            int rows_left, float scale) {
   typedef typename YType<Y>::T T;
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int j = 0; j < 2; ++j)
+    if (j < rows_left) {
+      T* y = static_cast<T*>(p.Y) + at + size_t(j) * p.ldy;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (m * 8 + j < rows_left) {
-        T* y = static_cast<T*>(p.Y) + at + size_t(m * 8 + j) * p.ldy;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i * 32] = YType<Y>::of(acc.v[m][i >> 1][(i & 1) * 2 + j] * scale);
-      }
+      for (int i = 0; i < 4; ++i) y[i * 32] = YType<Y>::of(acc.v[i >> 1][(i & 1) * 2 + j] * scale);
+    }
 }
 
 // First output of a lane-row: unit q (32 outputs), local output r.
@@ -373,34 +343,30 @@ __device__ __forceinline__ uint32_t stage_scales(const Stage* st) {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 8;                 // of a slot
+constexpr int kRing = 3;                 // steps of weight per warp: two in flight beside the one in use
+constexpr int kMaxUnits = 64;            // of a phase
+constexpr int kRedRow = kRows + 1;       // floats of an output's sums: one more against bank conflicts
+constexpr int kPart = kUnitRows * kRedRow;
+constexpr int kMaxSmem = 226 * 1024;     // 227 KB less the static part
 
-// Shared memory: rings; the warps' partial sums of their first and, for MT == 1, last unit
-// (for MT > 1 the last one's go into the warp's ring, which has run out by then); activations
+// Shared memory: rings; the warps' partial sums of their first and last unit; activations
 // [row][step], pitch 64 bytes over the steps' 256 (rows on other banks); their scalings; the
 // CTA's sums for the cluster; the experts' slots.
-constexpr int kMaxUnits = 64;  // of a phase
-template <int MT>
 struct Layout {
   int steps, rows, out_units, E;
-  // steps of weight per warp: one or two in flight beside the one in use
-  static constexpr int kRing = MT == 4 ? 2 : 3;
-  static constexpr int kRedRow = 8 * MT + 1;
-  static constexpr int kPart = kUnitRows * kRedRow;  // floats
   static constexpr int kRingBytes = int(sizeof(Stage)) * kRing * kWarps;
-  static constexpr int kX = kRingBytes + kWarps * (MT == 1 ? 2 : 1) * kPart * 4;
-  static_assert(MT == 1 || kPart * 4 <= int(sizeof(Stage)) * kRing, "the last unit's sums fit in the ring");
+  static constexpr int kX = kRingBytes + kWarps * 2 * kPart * 4;
   __host__ __device__ int pitch() const { return steps * (kStepK * 2) + 64; }
   __host__ __device__ int undo() const { return kX + rows * pitch(); }
-  __host__ __device__ int out() const { return undo() + steps * 8 * MT * 4; }
+  __host__ __device__ int out() const { return undo() + steps * kRows * 4; }
   __host__ __device__ int table() const { return out() + out_units * rows * kUnitRows * 4; }
-  __host__ __device__ int bytes() const { return table() + (E > 0 ? (E + 1) * 4 : 0); }
+  __host__ __device__ long long bytes() const { return (long long)table() + (E > 0 ? (E + 1) * 4 : 0); }
 };
 
-template <int MT, bool BF16, int VIEW>
+template <bool BF16, int VIEW>
 __global__ void __launch_bounds__(kThreads, 1)
-matvec_kernel(const MatvecParams p) {
-  typedef Layout<MT> L;
-  constexpr int kRing = L::kRing;
+stream_kernel(const MatvecParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int s_wide;
   __shared__ int s_span[kMaxUnits];  // warps that share a unit: first | last << 8 | (first one's which) << 16
@@ -409,16 +375,14 @@ matvec_kernel(const MatvecParams p) {
   const int cluster = S > 1 ? int(blockIdx.x) / S : int(blockIdx.x);
   const int clusters = S > 1 ? int(gridDim.x) / S : int(gridDim.x);
   const int s_begin = all_steps * rank / S, steps = all_steps * (rank + 1) / S - s_begin;
-  const L lay{(all_steps + S - 1) / S, p.x_rows, p.out_units, p.E};
+  const Layout lay{(all_steps + S - 1) / S, p.x_rows, p.out_units, p.E};
   // a warp's sums of its share's first unit (which 0) or last (1)
   auto part_of = [&](int w, int which) {
-    if (MT == 1) return reinterpret_cast<float*>(smem + L::kRingBytes) + (w * 2 + which) * L::kPart;
-    return which == 0 ? reinterpret_cast<float*>(smem + L::kRingBytes) + w * L::kPart
-                      : reinterpret_cast<float*>(smem + w * (int(sizeof(Stage)) * kRing));
+    return reinterpret_cast<float*>(smem + Layout::kRingBytes) + (w * 2 + which) * kPart;
   };
-  uint8_t* const s_x = smem + L::kX;
+  uint8_t* const s_x = smem + Layout::kX;
   float* const s_undo = reinterpret_cast<float*>(smem + lay.undo());
-  float* const s_out = reinterpret_cast<float*>(smem + lay.out());
+  float* const s_out = reinterpret_cast<float*>(smem + lay.out());  // [unit][row][32]
   int* const s_table = reinterpret_cast<int*>(smem + lay.table());  // [E + 1] slots before each expert
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -434,7 +398,7 @@ matvec_kernel(const MatvecParams p) {
       for (int base = 0; base < p.E; base += 32) {
         const int e = base + lane;
         const int rows = e < p.E ? p.offsets[e + 1] - p.offsets[e] : 0;
-        int incl = (rows + 8 * MT - 1) / (8 * MT);
+        int incl = (rows + kRows - 1) / kRows;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
@@ -447,7 +411,7 @@ matvec_kernel(const MatvecParams p) {
     }
     __syncthreads();
   }
-  const int slots = p.E > 0 ? s_table[p.E] : (p.M + 8 * MT - 1) / (8 * MT);
+  const int slots = p.E > 0 ? s_table[p.E] : 1;
   const long long all = (long long)slots * units;
   const int first = int(all * cluster / clusters), last = int(all * (cluster + 1) / clusters);
   auto expert_of = [&](int slot) {
@@ -465,31 +429,28 @@ matvec_kernel(const MatvecParams p) {
   };
 
   // The weight's stream: phase after phase, this warp's share of the phase's (unit, step) list
-  // in unit-major order. For MT > 1 it stops at the end of a phase, whose sums take the rings'
-  // place.
+  // in unit-major order.
   Stage* const ring = reinterpret_cast<Stage*>(smem) + warp * kRing;
   const uint32_t to_codes = ptx::smem_u32(&ring[0].codes[0][lane]), to_scales = stage_scales<VIEW>(ring);
   Source<VIEW> src;
   int f_next = first;       // unit that starts the next phase to fetch
   int f_at = 0, f_end = 0;  // next step of the phase's list, end of this warp's share
   int f_step = 0, f_unit = 0, f_e = 0;
-  auto fetch_phase = [&]() {
-    const int slot = f_next / units, end = phase_end(f_next, slot);
-    const unsigned n = unsigned(end - f_next) * unsigned(steps);
-    f_at = int(n * warp / kWarps);
-    f_end = int(n * (warp + 1) / kWarps);
-    if (f_at < f_end) {
-      const int unit = f_at / steps;
-      f_step = f_at - unit * steps;
-      f_unit = f_next - slot * units + unit;
-      f_e = expert_of(slot);
-      src.set(p, f_e, f_unit, s_begin + f_step);
-    }
-    f_next = end;
-  };
   auto fetch = [&](int to) {
-    if (MT == 1)
-      while (f_at == f_end && f_next < last) fetch_phase();  // a share of a short phase may be empty
+    while (f_at == f_end && f_next < last) {  // a share of a short phase may be empty
+      const int slot = f_next / units, end = phase_end(f_next, slot);
+      const unsigned n = unsigned(end - f_next) * unsigned(steps);
+      f_at = int(n * warp / kWarps);
+      f_end = int(n * (warp + 1) / kWarps);
+      if (f_at < f_end) {
+        const int unit = f_at / steps;
+        f_step = f_at - unit * steps;
+        f_unit = f_next - slot * units + unit;
+        f_e = expert_of(slot);
+        src.set(p, f_e, f_unit, s_begin + f_step);
+      }
+      f_next = end;
+    }
     if (f_at < f_end) {
       src.fetch(to_codes + to * uint32_t(sizeof(Stage)), to_scales + to * uint32_t(sizeof(Stage)), quarter);
       ++f_at;
@@ -500,16 +461,12 @@ matvec_kernel(const MatvecParams p) {
     }
     copies_commit();
   };
-  auto preload = [&]() {
-    if (MT > 1 && f_next < last) fetch_phase();
-#pragma unroll
-    for (int i = 0; i < kRing - 1; ++i) fetch(i);
-  };
   if (p.E == 0 && !p.early) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
   }
-  preload();
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) fetch(i);
   if (p.E == 0 && p.early) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -550,7 +507,7 @@ matvec_kernel(const MatvecParams p) {
           bool wide;
           v[b] = scale_bf16(v[b], &undo, &wide);
           if (c == 0 && at[b] >= 0) {
-            s_undo[ss * (8 * MT) + rr] = undo;
+            s_undo[ss * kRows + rr] = undo;
             if (wide) s_wide = 1;
           }
         }
@@ -571,8 +528,8 @@ matvec_kernel(const MatvecParams p) {
       slot = now;
       e = expert_of(slot);
       const int row_first = p.E > 0 ? p.offsets[e] : 0, row_last = p.E > 0 ? p.offsets[e + 1] : p.M;
-      row0 = row_first + (slot - (p.E > 0 ? s_table[e] : 0)) * 8 * MT;
-      rows = max(1, min(min(row_last, p.M) - row0, min(8 * MT, p.x_rows)));
+      row0 = row_first + (slot - (p.E > 0 ? s_table[e] : 0)) * kRows;
+      rows = max(1, min(min(row_last, p.M) - row0, p.x_rows));
       scale = p.w_scale[size_t(e) * 4];
       if (BF16) {
         if (threadIdx.x == 0) s_wide = 0;
@@ -595,105 +552,92 @@ matvec_kernel(const MatvecParams p) {
       const unsigned w0 = ((lo + 1) * kWarps - 1) / n, w1 = ((lo + steps) * kWarps - 1) / n;
       s_span[threadIdx.x] = int(w0 | w1 << 8 | (n * w0 / kWarps == lo ? 0u : 1u) << 16);
     }
-    // rows past the last read the first one's: their sums are never stored
+    // a row past the last reads the first one's: its sums are never stored
+    const uint8_t* const x_row = s_x + (g < rows ? g : 0) * lay.pitch() + t * 16;
     const int i_begin = int(n * warp / kWarps), i_end = int(n * (warp + 1) / kWarps);
     int unit = i_begin / steps;
     for (int i = i_begin, which = 0; i < i_end; ++unit, which = 1) {
       const int seg_end = min(i_end, (unit + 1) * steps);
       const bool whole = i == unit * steps && seg_end == (unit + 1) * steps;
-      Acc<MT> acc;
-      acc.clear();
-      for (int ls = i - unit * steps; i < seg_end; ++i, ++ls) {
+      Acc acc;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc.v[h][c] = 0.f;
+      for (int s = i - unit * steps; i < seg_end; ++i, ++s) {
         copies_wait<kRing - 2>();
         __syncwarp();  // the scale words come from four lanes; the stage before has been read
         fetch(pos == 0 ? kRing - 1 : pos - 1);
-        const uint8_t* x = s_x + ls * (kStepK * 2) + t * 16;
-        auto load_x = [&](int m, int q) {
-          const int r = m * 8 + g < rows ? m * 8 + g : 0;
-          return *reinterpret_cast<const uint4*>(x + r * lay.pitch() + q * 64);
-        };
+        const uint8_t* x = x_row + s * (kStepK * 2);
         if (BF16 && wide)
-          step_bf16<MT, VIEW>(acc, ring[pos], rows, load_x);
+          step_bf16<VIEW>(acc, ring[pos], x);
         else
-          step_f16<MT, VIEW, BF16>(acc, ring[pos], rows, load_x, [&](int m) {
-            return *reinterpret_cast<const float2*>(s_undo + ls * (8 * MT) + m * 8 + 2 * t);
-          });
+          step_f16<VIEW, BF16>(acc, ring[pos], x, s_undo + s * kRows + 2 * t);
         pos = pos + 1 == kRing ? 0 : pos + 1;
       }
-      if (MT > 1) __syncwarp();  // the ring has been read
       if (!whole) {
-        float* part = part_of(warp, which) + g * L::kRedRow + 2 * t;
+        float* part = part_of(warp, which) + g * kRedRow + 2 * t;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if (MT > 1 && m * 8 >= rows) break;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              part[(2 * h + (c >> 1)) * 8 * L::kRedRow + m * 8 + (c & 1)] = acc.v[m][h][c];
-        }
+          for (int c = 0; c < 4; ++c)
+            part[(2 * h + (c >> 1)) * 8 * kRedRow + (c & 1)] = acc.v[h][c];
       } else if (S > 1) {
         float* out = s_out + (unit * rows + 2 * t) * kUnitRows + g;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int j = 0; j < 2; ++j)
+          if (j < rows - 2 * t) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (m * 8 + j < rows - 2 * t) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                out[(m * 8 + j) * kUnitRows + i * 8] = acc.v[m][i >> 1][(i & 1) * 2 + j];
-            }
+            for (int i = 0; i < 4; ++i) out[j * kUnitRows + i * 8] = acc.v[i >> 1][(i & 1) * 2 + j];
+          }
       } else {
         const size_t y = size_t(row0 + 2 * t) * p.ldy + output_of(base + unit, g);
         if (p.y_dtype == SHARQ_BF16)
-          store_unit<MT, SHARQ_BF16>(p, acc, y, rows - 2 * t, scale);
+          store_unit<SHARQ_BF16>(p, acc, y, rows - 2 * t, scale);
         else if (p.y_dtype == SHARQ_F16)
-          store_unit<MT, SHARQ_F16>(p, acc, y, rows - 2 * t, scale);
+          store_unit<SHARQ_F16>(p, acc, y, rows - 2 * t, scale);
         else
-          store_unit<MT, SHARQ_F32>(p, acc, y, rows - 2 * t, scale);
+          store_unit<SHARQ_F32>(p, acc, y, rows - 2 * t, scale);
       }
     }
     __syncthreads();
 
     // units that several warps share, in the warps' order: a warp takes 32 outputs of a row
-    {
-      const int nu = end - at;
-      int u = warp, m = 0;
-      while (u >= nu && m < rows) { u -= nu; ++m; }
-      while (m < rows) {
-        const int span = s_span[u], w0 = span & 255, w1 = (span >> 8) & 255;
-        if (w0 != w1) {
-          float v = part_of(w0, span >> 16)[lane * L::kRedRow + m];
-          constexpr int kNext = (MT == 1 ? 2 : 1) * L::kPart;
-          const float* next = part_of(w0 + 1, 0) + lane * L::kRedRow + m;
-          if (n >= unsigned(kWarps)) {
-            for (int w = w1 - w0; w > 0; w -= 4, next += 4 * kNext) {
-              const float x0 = next[0], x1 = w > 1 ? next[kNext] : 0.f, x2 = w > 2 ? next[2 * kNext] : 0.f,
-                          x3 = w > 3 ? next[3 * kNext] : 0.f;
-              v += x0;
-              v += x1;
-              v += x2;
-              v += x3;
-            }
-          } else {  // fewer steps than warps: some shares are empty
-            for (int w = w0 + 1; w <= w1; ++w, next += kNext)
-              if (n * unsigned(w) / kWarps < n * unsigned(w + 1) / kWarps) v += *next;
+    const int nu = end - at;
+    int u = warp, m = 0;
+    while (u >= nu && m < rows) { u -= nu; ++m; }
+    while (m < rows) {
+      const int span = s_span[u], w0 = span & 255, w1 = (span >> 8) & 255;
+      if (w0 != w1) {
+        float v = part_of(w0, span >> 16)[lane * kRedRow + m];
+        constexpr int kNext = 2 * kPart;
+        const float* next = part_of(w0 + 1, 0) + lane * kRedRow + m;
+        if (n >= unsigned(kWarps)) {
+          for (int w = w1 - w0; w > 0; w -= 4, next += 4 * kNext) {
+            const float x0 = next[0], x1 = w > 1 ? next[kNext] : 0.f, x2 = w > 2 ? next[2 * kNext] : 0.f,
+                        x3 = w > 3 ? next[3 * kNext] : 0.f;
+            v += x0;
+            v += x1;
+            v += x2;
+            v += x3;
           }
-          if (S > 1)
-            s_out[(u * rows + m) * kUnitRows + lane] = v;
-          else
-            store_y(p, size_t(row0 + m) * p.ldy + output_of(base + u, lane), v * scale);
+        } else {  // fewer steps than warps: some shares are empty
+          for (int w = w0 + 1; w <= w1; ++w, next += kNext)
+            if (n * unsigned(w) / kWarps < n * unsigned(w + 1) / kWarps) v += *next;
         }
-        u += kWarps;
-        while (u >= nu && m < rows) { u -= nu; ++m; }
+        if (S > 1)
+          s_out[(u * rows + m) * kUnitRows + lane] = v;
+        else
+          store_y(p, size_t(row0 + m) * p.ldy + output_of(base + u, lane), v * scale);
       }
+      u += kWarps;
+      while (u >= nu && m < rows) { u -= nu; ++m; }
     }
     if (S > 1) {
       ptx::cluster_sync();
-      const int pairs = (end - at) * rows;
-      int u = 0, m = rank * kWarps + warp;
-      for (int i = m; i < pairs; i += S * kWarps, m += S * kWarps) {
-        while (m >= rows) { m -= rows; ++u; }
+      int cu = 0, cm = rank * kWarps + warp;
+      for (int i = cm; i < nu * rows; i += S * kWarps, cm += S * kWarps) {
+        while (cm >= rows) { cm -= rows; ++cu; }
         const uint32_t a = ptx::smem_u32(s_out + i * kUnitRows + lane);
         float v[8];
 #pragma unroll
@@ -704,36 +648,44 @@ matvec_kernel(const MatvecParams p) {
         float sum = v[0];
 #pragma unroll
         for (int c = 1; c < 8; ++c) sum += v[c];
-        store_y(p, size_t(row0 + m) * p.ldy + output_of(base + u, lane), sum * scale);
+        store_y(p, size_t(row0 + cm) * p.ldy + output_of(base + cu, lane), sum * scale);
       }
       ptx::cluster_sync();  // no CTA writes its sums again, or leaves, while they are read
     } else if (end < last) {
       __syncthreads();  // the slot's activations and sums have been read
     }
     at = end;
-    if (MT > 1 && at < last) {
-      pos = 0;
-      preload();
-    }
   }
   copies_wait<0>();
 }
 
 // ------------------------------------------------------------------------------ launch
 
-constexpr int kMaxSmem = 226 * 1024;  // 227 KB less the static part
+// K over as few CTAs as let the activations fit, beside the sums of at least two units; 0 where
+// not even eight do.
+int splits_for(int steps, int rows, int E) {
+  for (int S = 1; S <= 8 && S <= steps; S *= 2)
+    if (steps / S < 4096 && Layout{(steps + S - 1) / S, rows, S > 1 ? 2 : 0, E}.bytes() <= kMaxSmem) return S;
+  return 0;
+}
 
 // Clusters of S CTAs, one CTA per SM, that the current device runs at once.
 template <typename Kernel>
-cudaError_t max_clusters(Kernel* kern, int S, int smem, int num_sms, int* out) {
-  static std::atomic<int> known[4];  // by log2 S; every kernel here takes a whole SM
-  const int i = S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3;
-  *out = S == 1 ? num_sms : known[i].load(std::memory_order_relaxed);
-  if (*out > 0) return cudaSuccess;
+cudaError_t max_clusters(Kernel* kern, int S, int num_sms, unsigned long long ctx, int* out) {
+  struct Known {
+    std::atomic<unsigned long long> ctx{~0ull};
+    std::atomic<int> clusters{0};
+  };
+  static Known known[4];  // by log2 S; every kernel here takes a whole SM
+  Known& k = known[S == 2 ? 1 : S == 4 ? 2 : 3];
+  if (k.ctx.load(std::memory_order_acquire) == ctx) {
+    *out = k.clusters.load(std::memory_order_relaxed);
+    return cudaSuccess;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(num_sms / S * S));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.dynamicSmemBytes = kMaxSmem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = unsigned(S);
@@ -744,37 +696,34 @@ cudaError_t max_clusters(Kernel* kern, int S, int smem, int num_sms, int* out) {
   const cudaError_t e = cudaOccupancyMaxActiveClusters(out, kern, &cfg);
   if (e != cudaSuccess) return e;
   if (*out < 1) return cudaErrorInvalidConfiguration;
-  known[i].store(*out, std::memory_order_relaxed);
+  k.clusters.store(*out, std::memory_order_relaxed);
+  k.ctx.store(ctx, std::memory_order_release);
   return cudaSuccess;
 }
 
-template <int MT, bool BF16, int VIEW>
-cudaError_t launch_mt(MatvecParams p, int num_sms, unsigned long long ctx, cudaStream_t st) {
-  // K over as few CTAs as let the activations fit, beside the sums of at least two units
+template <bool BF16, int VIEW>
+cudaError_t launch_stream(MatvecParams p, int num_sms, unsigned long long ctx, cudaStream_t st) {
   const int steps = p.K / kStepK;
-  int S = 1;
-  for (;; S *= 2) {
-    if (S > 8 || S > steps) return cudaErrorInvalidConfiguration;  // excluded by launch_view
-    if (Layout<MT>{(steps + S - 1) / S, p.x_rows, S > 1 ? 2 : 0, p.E}.bytes() <= kMaxSmem) break;
-  }
-  p.splits = S;
+  p.x_rows = p.E > 0 ? kRows : p.M;
+  p.splits = splits_for(steps, p.x_rows, p.E);
   p.out_units = 0;
-  Layout<MT> lay{(steps + S - 1) / S, p.x_rows, 0, p.E};
-  if (S > 1) {
-    p.out_units = (kMaxSmem - lay.bytes()) / (p.x_rows * kUnitRows * 4);
-    if (p.out_units > p.N / kUnitRows) p.out_units = p.N / kUnitRows;
-    lay.out_units = p.out_units;
-  }
-  auto* kern = matvec_kernel<MT, BF16, VIEW>;
+  if (p.splits == 0) return cudaErrorInvalidConfiguration;
+  Layout lay{(steps + p.splits - 1) / p.splits, p.x_rows, 0, p.E};
+  int clusters = num_sms;
+  auto* kern = stream_kernel<BF16, VIEW>;
   static std::atomic<unsigned long long> done{~0ull};
   cudaError_t e = allow_smem(kern, kMaxSmem, ctx, &done);
   if (e != cudaSuccess) return e;
-  int clusters = 0;
-  if ((e = max_clusters(kern, S, lay.bytes(), num_sms, &clusters)) != cudaSuccess) return e;
-  const long long units = (long long)(p.N / kUnitRows) * (p.E > 0 ? p.M : (p.M + 8 * MT - 1) / (8 * MT));
+  if (p.splits > 1) {
+    const int most = int((kMaxSmem - lay.bytes()) / (p.x_rows * kUnitRows * 4));
+    p.out_units = most < kMaxUnits ? most : kMaxUnits;
+    lay.out_units = p.out_units;
+    if ((e = max_clusters(kern, p.splits, num_sms, ctx, &clusters)) != cudaSuccess) return e;
+  }
+  const long long units = (long long)(p.N / kUnitRows) * (p.E > 0 ? p.M : 1);
   if (units < clusters) clusters = int(units);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(clusters * S));
+  cfg.gridDim = dim3(unsigned(clusters * p.splits));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = size_t(lay.bytes());
   cfg.stream = st;
@@ -782,50 +731,30 @@ cudaError_t launch_mt(MatvecParams p, int num_sms, unsigned long long ctx, cudaS
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = unsigned(S);
+  attr[1].val.clusterDim.x = unsigned(p.splits);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = S > 1 ? 2 : 1;
+  cfg.numAttrs = p.splits > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <bool BF16, int VIEW>
-cudaError_t launch_view(MatvecParams p, int num_sms, unsigned long long ctx, cudaStream_t st) {
-  // Rows per slot: 8 to 32. An expert's rows are not known here, twice their mean stands for
-  // them.
-  const int per = p.E > 0 ? 2 * ((p.M + p.E - 1) / p.E) : p.M;
-  const int steps = p.K / kStepK, eighth = (steps + 7) / 8;
-  int mt = per <= 8 ? 1 : per <= 16 ? 2 : per <= 24 ? 3 : 4;
-  auto fits = [&](int m) {
-    const int rows = p.E == 0 && p.M < 8 * m ? p.M : 8 * m;
-    return (m == 4   ? Layout<4>{eighth, rows, 2, p.E}.bytes()
-            : m == 3 ? Layout<3>{eighth, rows, 2, p.E}.bytes()
-            : m == 2 ? Layout<2>{eighth, rows, 2, p.E}.bytes()
-                     : Layout<1>{eighth, rows, 2, p.E}.bytes()) <= kMaxSmem;
-  };
-  while (mt > 1 && !fits(mt)) --mt;
-  if (!fits(mt)) return cudaErrorInvalidConfiguration;  // K is bounded by the caller's checks
-  p.x_rows = p.E == 0 && p.M < 8 * mt ? p.M : 8 * mt;
-  switch (mt) {
-    case 1: return launch_mt<1, BF16, VIEW>(p, num_sms, ctx, st);
-    case 2: return launch_mt<2, BF16, VIEW>(p, num_sms, ctx, st);
-    case 3: return launch_mt<3, BF16, VIEW>(p, num_sms, ctx, st);
-    default: return launch_mt<4, BF16, VIEW>(p, num_sms, ctx, st);
-  }
-}
-
 }  // namespace
+
+bool matvec_streams(int M, int E, int K) {
+  if (E > 0 ? M > 4 * E : M > kRows) return false;
+  return splits_for(K / kStepK, E > 0 ? kRows : M, E) > 0;
+}
 
 cudaError_t launch_matvec(const MatvecParams& p, bool bf16, ScaleView view, int num_sms,
                           unsigned long long ctx, cudaStream_t st) {
   switch (view) {
     case kE4M3x16:
-      return bf16 ? launch_view<true, kE4M3x16>(p, num_sms, ctx, st) : launch_view<false, kE4M3x16>(p, num_sms, ctx, st);
+      return bf16 ? launch_stream<true, kE4M3x16>(p, num_sms, ctx, st) : launch_stream<false, kE4M3x16>(p, num_sms, ctx, st);
     case kE4M3x32:
-      return bf16 ? launch_view<true, kE4M3x32>(p, num_sms, ctx, st) : launch_view<false, kE4M3x32>(p, num_sms, ctx, st);
+      return bf16 ? launch_stream<true, kE4M3x32>(p, num_sms, ctx, st) : launch_stream<false, kE4M3x32>(p, num_sms, ctx, st);
     default:
-      return bf16 ? launch_view<true, kE8M0x32>(p, num_sms, ctx, st) : launch_view<false, kE8M0x32>(p, num_sms, ctx, st);
+      return bf16 ? launch_stream<true, kE8M0x32>(p, num_sms, ctx, st) : launch_stream<false, kE8M0x32>(p, num_sms, ctx, st);
   }
 }
 

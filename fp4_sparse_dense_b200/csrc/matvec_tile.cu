@@ -16,7 +16,7 @@
 // carries 2^-8 until the end; E8M0 * E2M1 as it is). fp16 activations beside E8M0 scales, which
 // may leave f16's range, enter as two bf16 (8 + 3 bits), each in an MMA of its own.
 // The tensor core cuts an accumulator's bits below the 24th at every addition, so an accumulator
-// lives for two steps (16 MMAs) of one half of the widening warps: before those warps fill the
+// lives for three steps (24 MMAs) of one half of the widening warps: before those warps fill the
 // next operand, which they may only do when the MMAs of the last one have completed, they add
 // it to float32 sums, rounding to nearest. The sums stay in tensor memory as well.
 //
@@ -41,13 +41,13 @@ constexpr int kWidenWarps = 8;
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kLoadWarp = 10, kLoadThreads = 128;
 constexpr int kTileThreads = (kLoadWarp + kLoadThreads / 32) * 32;
 constexpr int kWRing = 6;
-constexpr int kGroup = 2;  // steps of a half that share an accumulator
+constexpr int kGroup = 3;  // steps of a half that share an accumulator
 
 template <int NC, int OPS, int VIEW>
 struct Tile {
   static constexpr int kXTile = NC * 256;  // activations of a step: two swizzle atoms of 64 K
   static constexpr int kXStage = OPS == kF16AsTwoBF16 ? 2 * kXTile : kXTile;
-  static constexpr int kXRing = kXStage >= 16384 ? 2 : 4;
+  static constexpr int kXRing = kXStage >= 16384 ? 3 : 6;
   static constexpr int kWStage = 8192 + 1024;  // codes, scales (512 or 1024), 1 KB aligned
   static constexpr int kSmem = kXRing * kXStage + kWRing * kWStage + 1024;
   // tensor memory: two accumulators, two sums, two operand buffers of 64 columns
@@ -417,30 +417,34 @@ tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
       // an operand's descriptor is the first stage's plus its offset in 16-byte units, which never
       // leaves the address field
       const uint64_t desc = ptx::smem_desc(ptx::smem_u32(s_x), 16, 1024, 2);
-      int own[2] = {0, 0};  // steps of each half in the tile
-      for (int g = 0, i = 0; g < total; ++g) {
-        const int st = g % XR, half = g & 1;
-        if (!ptx::mbar_wait(bar(x_full + st), (g / XR) & 1, abort_flag, limit) ||
-            !ptx::mbar_wait(bar(a_full + half), (g >> 1) & 1, abort_flag, limit)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
+      // Everything but the wait for the operand comes before it: this thread's instructions between
+      // the operand's arrival and the MMAs are part of every step's latency.
+      int st = 0, i = 0;
+      uint32_t x_phase = 0, own0 = 0, own1 = 0;  // own: steps of each half in the tile
+      auto step = [&](int half, uint32_t a_phase, uint32_t& own) {
         const uint32_t d = tbase + half * NC, a = tbase + C::kColA + half * 64;
         const uint64_t x = desc + uint32_t(st * (C::kXStage >> 4));
-        uint32_t acc = (half ? own[1] : own[0]) % kGroup != 0 ? 1u : 0u;
+        const uint32_t x_bar = bar(x_empty + st), first_acc = own % kGroup != 0 ? 1u : 0u;
+        if (!ptx::mbar_wait(bar(x_full + st), x_phase, abort_flag, limit) ||
+            !ptx::mbar_wait(bar(a_full + half), a_phase, abort_flag, limit))
+          return false;
+        ptx::tc_fence_after();
 #pragma unroll
         for (int t = 0; t < (OPS == kF16AsTwoBF16 ? 2 : 1); ++t)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 8; ++j)
             mma_ts(d, a + j * 8, x + uint32_t((t * C::kXTile + (j >> 2) * (NC * 128) + (j & 3) * 32) >> 4),
-                   idesc, acc);
-            acc = 1u;
-          }
+                   idesc, t + j == 0 ? first_acc : 1u);
         ptx::mma_commit(bar(a_empty + half));
-        ptx::mma_commit(bar(x_empty + st));
-        if (half) ++own[1]; else ++own[0];
-        if (++i == steps) i = own[0] = own[1] = 0;
+        ptx::mma_commit(x_bar);
+        ++own;
+        if (++i == steps) i = 0, own0 = own1 = 0;
+        if (++st == XR) st = 0, x_phase ^= 1u;
+        return true;
+      };
+      for (int g = 0; g < total && ok; g += 2) {
+        ok = step(0, (g >> 1) & 1, own0);
+        if (ok && g + 1 < total) ok = step(1, (g >> 1) & 1, own1);
       }
       // every MMA issued above has completed before the CTA leaves
       for (int g = total > 2 ? total - 2 : 0; g < total && ok; ++g)
@@ -452,7 +456,9 @@ tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
     const uint16_t* src[NC / 8];
     // 16-byte unit c of row r: atom c / 8 (64 K), unit (c % 8) ^ (r % 8)
     const uint32_t to = (c >> 3) * (NC * 128) + r8 * 128 + (((c & 7) ^ r8) << 4);
-    constexpr int kAhead = XR - 1;
+    // a step's copies have kAhead steps to land, and are asked for XR - kAhead steps before the
+    // MMAs that free their place: the one that is being filled is never waited for
+    constexpr int kAhead = XR / 3;
     int x_tile = first, x_step = 0;  // next step to copy
     for (int g = 0; g < total + kAhead; ++g) {
       if (g < total) {

@@ -468,7 +468,7 @@ sharq_status matvec_weight(const void* X, size_t ldx, sharq_dtype dtype, void* c
 sharq_status run_matvec(MatvecParams* p, bool bf16, ScaleView view, const DeviceInfo& d,
                         cudaStream_t st) {
   CUtensorMap map;
-  const bool tiles = matvec_by_tiles(p->M, p->E);
+  const bool tiles = !matvec_streams(p->M, p->E, p->K);
   if (tiles) {
     const sharq_status s = make_map(&map, p->codes, uint64_t(p->K) / 2,
                                     uint64_t(p->N) * uint64_t(p->E > 0 ? p->E : 1), 64, 128,
