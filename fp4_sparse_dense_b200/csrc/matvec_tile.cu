@@ -616,12 +616,13 @@ cudaError_t launch_matvec_tiles(const CUtensorMap& map, MatvecParams p, bool bf1
   unsigned slots = unsigned((p.M + nc - 1) / nc);
   double busy = slots;
   if (p.E > 0) {
-    // sum over experts of ceil(rows / nc) <= experts with rows + M / nc
+    // sum over experts of ceil(rows / nc) <= experts with rows + M / nc; about one each while
+    // nc holds twice the mean
     const int used = p.E < p.M ? p.E : p.M;
     slots = unsigned(used + p.M / nc);
-    busy = used + 0.5 * (p.M / nc);
+    const double full = double(p.M) / nc + 0.5 * used;
+    busy = full > used ? full : used;
   }
-  if (slots > 65535u) return cudaErrorInvalidConfiguration;  // bounded by the caller's checks
   // K over a cluster of S CTAs, four steps each at least, where that gives the least time: S == 1
   // shares whole tiles out over the CTAs that run at once, S > 1 pays a CTA's start and end
   // (about 6 steps) in every round.
@@ -630,7 +631,7 @@ cudaError_t launch_matvec_tiles(const CUtensorMap& map, MatvecParams p, bool bf1
   auto rounds = [](double n) { return double((long long)(n + 0.999)); };
   double best = rounds(tiles / run) * steps + 6.0;
   p.splits = 1;
-  for (int S = 2; S <= 8 && S * 4 <= steps; S *= 2) {
+  for (int S = 2; S <= 8 && S * 4 <= steps && slots <= 65535u; S *= 2) {
     const double cost = rounds(tiles * S / run) * (double(steps) / S + 6.0);
     if (cost < best) {
       best = cost;
