@@ -38,6 +38,7 @@
 // an accumulator lives for one step (8 MMAs) and joins a float32 sum that rounds to nearest.
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -352,7 +353,7 @@ constexpr int kMaxSmem = 226 * 1024;     // 227 KB less the static part
 
 // Shared memory: rings; the warps' partial sums of their first and last unit; activations
 // [row][step], pitch 64 bytes over the steps' 256 (rows on other banks); their scalings; the
-// CTA's sums for the cluster; the experts' slots.
+// CTA's sums for the cluster; the experts' slots and offsets.
 struct Layout {
   int steps, rows, out_units, E;
   static constexpr int kRingBytes = int(sizeof(Stage)) * kRing * kWarps;
@@ -361,14 +362,13 @@ struct Layout {
   __host__ __device__ int undo() const { return kX + rows * pitch(); }
   __host__ __device__ int out() const { return undo() + steps * kRows * 4; }
   __host__ __device__ int table() const { return out() + out_units * rows * kUnitRows * 4; }
-  __host__ __device__ long long bytes() const { return (long long)table() + (E > 0 ? (E + 1) * 4 : 0); }
+  __host__ __device__ long long bytes() const { return (long long)table() + (E > 0 ? (E + 1) * 8 : 0); }
 };
 
 template <bool BF16, int VIEW>
 __global__ void __launch_bounds__(kThreads, 1)
 stream_kernel(const MatvecParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_wide;
   __shared__ int s_span[kMaxUnits];  // warps that share a unit: first | last << 8 | (first one's which) << 16
   const int all_steps = p.K / kStepK, S = p.splits;
   const int rank = S > 1 ? int(blockIdx.x) % S : 0;
@@ -384,8 +384,9 @@ stream_kernel(const MatvecParams p) {
   float* const s_undo = reinterpret_cast<float*>(smem + lay.undo());
   float* const s_out = reinterpret_cast<float*>(smem + lay.out());  // [unit][row][32]
   int* const s_table = reinterpret_cast<int*>(smem + lay.table());  // [E + 1] slots before each expert
+  int* const s_offsets = s_table + p.E + 1;                          // [E + 1] rows before it
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int units = p.N / kUnitRows;  // per slot
   const size_t quarter = size_t(32) * (p.K / 2);
@@ -393,11 +394,14 @@ stream_kernel(const MatvecParams p) {
   if (p.E > 0) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    // one load latency for all of the offsets, then slots before each expert from shared memory
+    for (int i = threadIdx.x; i <= p.E; i += kThreads) s_offsets[i] = p.offsets[i];
+    __syncthreads();
     if (warp == 0) {
       int before = 0;
       for (int base = 0; base < p.E; base += 32) {
         const int e = base + lane;
-        const int rows = e < p.E ? p.offsets[e + 1] - p.offsets[e] : 0;
+        const int rows = e < p.E ? s_offsets[e + 1] - s_offsets[e] : 0;
         int incl = (rows + kRows - 1) / kRows;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -412,8 +416,11 @@ stream_kernel(const MatvecParams p) {
     __syncthreads();
   }
   const int slots = p.E > 0 ? s_table[p.E] : 1;
-  const long long all = (long long)slots * units;
-  const int first = int(all * cluster / clusters), last = int(all * (cluster + 1) / clusters);
+  // an equal run of all units (fewer than 2^31), the first CTAs one more
+  const unsigned all = unsigned(slots) * unsigned(units);
+  const unsigned run = all / unsigned(clusters), more = all - run * unsigned(clusters);
+  const int first = int(run * cluster + min(unsigned(cluster), more));
+  const int last = first + int(run + (unsigned(cluster) < more ? 1u : 0u));
   auto expert_of = [&](int slot) {
     if (p.E == 0) return 0;
     int lo = 0, hi = p.E;  // the last e with table[e] <= slot
@@ -465,7 +472,7 @@ stream_kernel(const MatvecParams p) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
   }
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kRing - 1; ++i) fetch(i);
   if (p.E == 0 && p.early) {
     ptx::griddep_wait();
@@ -480,6 +487,7 @@ stream_kernel(const MatvecParams p) {
     int r = 0, s = group;  // next (row, step) of the group
     while (s >= steps && r < rows) { s -= steps; ++r; }
     const int group2 = group & ~1;  // the warp's other half may have one more
+    bool any_wide = false;
     int left = rows * steps > group2 ? (rows * steps - group2 + kGroups - 1) / kGroups : 0;
     while (left > 0) {
       uint4 v[kBatch];
@@ -508,7 +516,7 @@ stream_kernel(const MatvecParams p) {
           v[b] = scale_bf16(v[b], &undo, &wide);
           if (c == 0 && at[b] >= 0) {
             s_undo[ss * kRows + rr] = undo;
-            if (wide) s_wide = 1;
+            any_wide |= wide;
           }
         }
         if (at[b] >= 0)
@@ -517,6 +525,7 @@ stream_kernel(const MatvecParams p) {
       }
       left -= kBatch;
     }
+    return any_wide;
   };
 
   int pos = 0, slot = -1, e = 0, row0 = 0, rows = 0;
@@ -527,19 +536,12 @@ stream_kernel(const MatvecParams p) {
     if (now != slot) {
       slot = now;
       e = expert_of(slot);
-      const int row_first = p.E > 0 ? p.offsets[e] : 0, row_last = p.E > 0 ? p.offsets[e + 1] : p.M;
+      const int row_first = p.E > 0 ? s_offsets[e] : 0, row_last = p.E > 0 ? s_offsets[e + 1] : p.M;
       row0 = row_first + (slot - (p.E > 0 ? s_table[e] : 0)) * kRows;
       rows = max(1, min(min(row_last, p.M) - row0, p.x_rows));
       scale = p.w_scale[size_t(e) * 4];
-      if (BF16) {
-        if (threadIdx.x == 0) s_wide = 0;
-        __syncthreads();
-      }
-      stage_x(row0, rows, BF16);
-      __syncthreads();
-      wide = BF16 && s_wide;
-      if (wide) {
-        __syncthreads();
+      wide = __syncthreads_or(stage_x(row0, rows, BF16)) != 0;
+      if (BF16 && wide) {
         stage_x(row0, rows, false);
         __syncthreads();
       }
@@ -564,16 +566,23 @@ stream_kernel(const MatvecParams p) {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc.v[h][c] = 0.f;
-      for (int s = i - unit * steps; i < seg_end; ++i, ++s) {
-        copies_wait<kRing - 2>();
-        __syncwarp();  // the scale words come from four lanes; the stage before has been read
-        fetch(pos == 0 ? kRing - 1 : pos - 1);
-        const uint8_t* x = x_row + s * (kStepK * 2);
-        if (BF16 && wide)
-          step_bf16<VIEW>(acc, ring[pos], x);
-        else
-          step_f16<VIEW, BF16>(acc, ring[pos], x, s_undo + s * kRows + 2 * t);
-        pos = pos + 1 == kRing ? 0 : pos + 1;
+      auto run = [&](auto as_bf16) {
+        for (int s = i - unit * steps; i < seg_end; ++i, ++s) {
+          copies_wait<kRing - 2>();
+          __syncwarp();  // the scale words come from four lanes; the stage before has been read
+          fetch(pos == 0 ? kRing - 1 : pos - 1);
+          const uint8_t* x = x_row + s * (kStepK * 2);
+          if constexpr (decltype(as_bf16)::value)
+            step_bf16<VIEW>(acc, ring[pos], x);
+          else
+            step_f16<VIEW, BF16>(acc, ring[pos], x, s_undo + s * kRows + 2 * t);
+          pos = pos + 1 == kRing ? 0 : pos + 1;
+        }
+      };
+      if constexpr (BF16) {
+        if (wide) run(std::true_type()); else run(std::false_type());
+      } else {
+        run(std::false_type());
       }
       if (!whole) {
         float* part = part_of(warp, which) + g * kRedRow + 2 * t;
@@ -742,7 +751,7 @@ cudaError_t launch_stream(MatvecParams p, int num_sms, unsigned long long ctx, c
 }  // namespace
 
 bool matvec_streams(int M, int E, int K) {
-  if (E > 0 ? M > 4 * E : M > kRows) return false;
+  if (E > 0 ? M > kRows * E : M > kRows) return false;
   return splits_for(K / kStepK, E > 0 ? kRows : M, E) > 0;
 }
 

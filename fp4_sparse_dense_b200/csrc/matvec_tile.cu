@@ -169,7 +169,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
   __shared__ int s_abort;
   volatile int* const abort_flag = &s_abort;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
   const int S = p.splits, nbs = p.N / 128;
   const int all_steps = p.K / kStepK;
   const int rank = S > 1 ? int(blockIdx.x) % S : 0;
@@ -201,7 +201,6 @@ tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
   if (warp == kCopyWarp && lane == 0) ptx::prefetch_tensormap(&map);
   if (p.E > 0) {
     ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
     if (warp == 0) {
       int before = 0;
       for (int base = 0; base < p.E; base += 32) {
@@ -223,6 +222,8 @@ tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tbase = s_tmem;
+  // a dependent's CTAs, which may allocate tensor memory too, come after this CTA's allocation
+  if (p.E > 0) ptx::griddep_launch_dependents();
 
   // the CTA's tiles: first, first + stride, ... below end (slot-major)
   const int slots = p.E > 0 ? s_table[p.E] : (p.M + NC - 1) / NC;
@@ -442,13 +443,15 @@ tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
         if (++st == XR) st = 0, x_phase ^= 1u;
         return true;
       };
-      for (int g = 0; g < total && ok; g += 2) {
-        ok = step(0, (g >> 1) & 1, own0);
-        if (ok && g + 1 < total) ok = step(1, (g >> 1) & 1, own1);
+      int issued = 0;
+      for (; issued < total && ok; issued += ok)
+        ok = step(issued & 1, (issued >> 1) & 1, issued & 1 ? own1 : own0);
+      // every MMA issued above has completed before the CTA leaves, after a timeout too
+      for (int g = issued > 2 ? issued - 2 : 0; g < issued; ++g) {
+        const uint64_t t0 = ptx::globaltimer();
+        while (!ptx::mbar_try_wait(bar(a_empty + (g & 1)), (g >> 1) & 1))
+          if (ptx::globaltimer() - t0 > limit) { ok = false; break; }
       }
-      // every MMA issued above has completed before the CTA leaves
-      for (int g = total > 2 ? total - 2 : 0; g < total && ok; ++g)
-        if (!ptx::mbar_wait(bar(a_empty + (g & 1)), (g >> 1) & 1, abort_flag, limit)) ok = false;
     }
   } else {
     // ------------------------------------------------------------------ the activations
@@ -523,6 +526,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map, const MatvecParams p) {
     atomicExch(p.status, unsigned(SHARQ_ERR_TIMEOUT));
   }
 
+  __syncwarp();
   if (S > 1) {
     ptx::cluster_sync();
     if (total > 0) {

@@ -810,7 +810,7 @@ sharq_status sharq_expert_matvec(const void* X, size_t ldx, int32_t gather, shar
                     w->K, w->N, w->cfg, Y, ldy, y_dtype, &p, &view);
   if (s != SHARQ_OK) return s;
   p.M = t->T * t->k;
-  if (p.M > (1 << 19)) return SHARQ_ERR_UNSUPPORTED;
+  if (p.M > (1 << 19) || (long long)w->E * w->N > INT32_MAX) return SHARQ_ERR_UNSUPPORTED;
   p.E = w->E;
   p.k = t->k;
   p.offsets = t->offsets;
