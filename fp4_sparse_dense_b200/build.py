@@ -8,6 +8,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,7 +25,6 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC,-O2,-fvisibility=hidden",
-    "-shared", "-cudart", "static",
     "--expt-relaxed-constexpr",
 ]
 
@@ -42,20 +43,28 @@ def _newest_input() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _run(cmd: list[str]) -> subprocess.CompletedProcess:
+    return subprocess.run(cmd, capture_output=True, text=True)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     os.makedirs(LIB_DIR, exist_ok=True)
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
         return LIB
     tmp = LIB + ".tmp"
-    cmd = [nvcc(), *NVCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"),
-           "-o", tmp, *[os.path.join(CSRC, f) for f in SOURCES]]
-    if verbose:
-        print(" ".join(cmd))
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
-    if verbose and (r.stdout or r.stderr):
-        print(r.stdout, r.stderr)
+    base = [nvcc(), *NVCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include")]
+    # the sources do not depend on one another: one nvcc each, a link at the end
+    with tempfile.TemporaryDirectory() as objects, ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+        objs = [os.path.join(objects, f[:-3] + ".o") for f in SOURCES]
+        cmds = [[*base, "-c", "-o", o, os.path.join(CSRC, f)] for f, o in zip(SOURCES, objs)]
+        link = [*base, "-shared", "-cudart", "static", "-o", tmp, *objs]
+        for cmd, r in [*zip(cmds, pool.map(_run, cmds)), (link, _run(link))]:
+            if verbose:
+                print(" ".join(cmd))
+                if r.stdout or r.stderr:
+                    print(r.stdout, r.stderr)
+            if r.returncode != 0:
+                raise RuntimeError(f"nvcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     return LIB
 
