@@ -16,11 +16,24 @@
 // memory, in a fixed order.
 //
 // The grid is one CTA per SM. A CTA keeps the activations of its slot (up to 8 rows of one
-// weight) in shared memory, read and converted once, and takes an equal run of the list of
-// 32-output units; its warps split the run's steps evenly, whatever unit they belong to, so
-// that there is one prologue and one sum per CTA and slot. Where the activations do not fit, a
-// cluster of S CTAs splits K, works through the same units and adds its sums through
-// distributed shared memory. More rows go to tile_kernel (matvec_tile.cu).
+// weight, or 16 with two MMAs per operand) in shared memory, read and converted once, and takes
+// an equal run of the list of 32-output units; its warps split the run's steps evenly, whatever
+// unit they belong to, so that there is one prologue and one sum per CTA and slot. The warp that
+// has a unit's first step keeps its sums in registers and adds those of the warps behind it.
+// Where the activations do not fit, a cluster of S CTAs splits K, works through the same units
+// and adds its sums through distributed shared memory; the fewest CTAs that fit, since more only
+// move the cost (14336 x 4096 bf16, 4 rows: 15.1 us with one, 15.2 with two, 14.4 with four,
+// 15.3 with eight; 4096 x 28672: 18.2, 20.3, 21.2, 23.7). More rows go to tile_kernel
+// (matvec_tile.cu).
+//
+// Measured (B200, weights cycling through more than L2 or nearly so; N x K/2 codes and scales
+// over time): 4096 x 28672 NVFP4 / 16, 1 row 14.8 us (4.5 TB/s); 14336 x 4096, 8 rows 13.5 us
+// (2.3 TB/s); 4096 x 4096, 1 row 5.3 us (1.7 TB/s). The loop runs near memory rate; what remains
+// is the start (launch, activations, the first weights: about 3 us) and the sums and stores
+// (about 1 us), which a short weight cannot hide. The code that runs once per launch comes cold
+// from L2, so it is kept short: branches that depend on a vote or a shuffled warp index, known
+// to be uniform, took gate_up from 17.5 to 14.9 us, the prologue's copies in a loop another 0.2
+// us.
 //
 // The widening sets the kernel's issue rate, so it uses the conversion instruction (two codes
 // to f16x2) and one packed multiply by the scale. That makes the weight an f16 operand:
@@ -38,7 +51,6 @@
 // an accumulator lives for one step (8 MMAs) and joins a float32 sum that rounds to nearest.
 #include <atomic>
 #include <cstdint>
-#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -130,8 +142,9 @@ struct Acc {
 
 // One step with f16 operands. x: the lane's row at its K unit 4 t of the step, unit 4 t + q 64 q
 // bytes on; undo: what takes the scaling of rows 2 t and 2 t + 1 out.
-template <int VIEW, bool SCALED>
-__device__ __forceinline__ void step_f16(Acc& acc, const Stage& st, const uint8_t* x, const float* undo) {
+template <int MT, int VIEW, bool SCALED>
+__device__ __forceinline__ void step_f16(Acc (&acc)[MT], const Stage& st, const uint8_t* const (&x)[MT], int x_at,
+                                         const float* undo) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t pick = uint32_t(t) | uint32_t(4 + t) << 4;  // byte t of two words
   const uint4 sv = st.scales[VIEW == kE4M3x16 ? t >> 1 : 0][g];
@@ -193,7 +206,7 @@ __device__ __forceinline__ void step_f16(Acc& acc, const Stage& st, const uint8_
         f[i][1] = f[i][0];
       }
     }
-    float part[2][4];
+    float part[MT][2][4];
     const uint4 cw[4] = {st.codes[0][lane], st.codes[1][lane], st.codes[2][lane], st.codes[3][lane]};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -205,37 +218,43 @@ __device__ __forceinline__ void step_f16(Acc& acc, const Stage& st, const uint8_
 #pragma unroll
         for (int j = 0; j < 4; ++j) a[i][j] = mul_f16x2(a[i][j], f[i][q >> 1]);
       }
-      const uint4 b = *reinterpret_cast<const uint4*>(x + q * 64);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (q == 0)
-          mma_f16_first(part[h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
-        else
-          mma_f16(part[h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
-        mma_f16(part[h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
+      for (int m = 0; m < MT; ++m) {
+        const uint4 b = *reinterpret_cast<const uint4*>(x[m] + x_at + q * 64);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (q == 0)
+            mma_f16_first(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
+          else
+            mma_f16(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
+          mma_f16(part[m][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
+        }
       }
     }
-    float2 out = make_float2(1.f, 1.f);
-    if (SCALED) out = *reinterpret_cast<const float2*>(undo);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int m = 0; m < MT; ++m) {
+      float2 out = make_float2(1.f, 1.f);
+      if (SCALED) out = *reinterpret_cast<const float2*>(undo + m * 8);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float v = part[h][c], o = c & 1 ? out.y : out.x;
-        float& to = acc.v[h][c];
-        if (VIEW == kE8M0x32)
-          to = fmaf(SCALED ? v * o : v, ref[2 * h + (c >> 1)], to);
-        else
-          to = SCALED ? fmaf(v, o, to) : to + v;
-      }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float v = part[m][h][c], o = c & 1 ? out.y : out.x;
+          float& to = acc[m].v[h][c];
+          if (VIEW == kE8M0x32)
+            to = fmaf(SCALED ? v * o : v, ref[2 * h + (c >> 1)], to);
+          else
+            to = SCALED ? fmaf(v, o, to) : to + v;
+        }
+    }
   } while (VIEW == kE8M0x32 && ++wp < wpasses);
 }
 
 // One step with bf16 operands: the widened codes' 2^-126 is taken out by the scale's factor
 // (E4M3: sf * 2^118, finite up to 448; E8M0: 2^(126 + b - b_max)), the rest with the sum.
 // The codes go in step_f16's order, so that both kinds of operands give the same bits.
-template <int VIEW>
-__device__ __forceinline__ void step_bf16(Acc& acc, const Stage& st, const uint8_t* x) {
+template <int MT, int VIEW>
+__device__ __forceinline__ void step_bf16(Acc (&acc)[MT], const Stage& st, const uint8_t* const (&x)[MT], int x_at) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint4 sv = st.scales[VIEW == kE4M3x16 ? t >> 1 : 0][g];
   const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
@@ -262,11 +281,9 @@ __device__ __forceinline__ void step_bf16(Acc& acc, const Stage& st, const uint8
       ref[i] = 256.f;
     }
   }
-  float part[2][4];
+  float part[MT][2][4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) part[h][c] = 0.f;
+  for (int i = 0; i < MT * 8; ++i) part[i >> 3][(i >> 2) & 1][i & 3] = 0.f;
 #pragma unroll 1
   for (int q = 0; q < 4; ++q) {
     uint32_t a[4][4];
@@ -281,17 +298,23 @@ __device__ __forceinline__ void step_bf16(Acc& acc, const Stage& st, const uint8
       a[i][2] = __byte_perm(h[0], h[1], 0x7632);
       a[i][3] = __byte_perm(h[2], h[3], 0x7632);
     }
-    const uint4 b = *reinterpret_cast<const uint4*>(x + q * 64);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      mma_bf16(part[h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
-      mma_bf16(part[h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
+    for (int m = 0; m < MT; ++m) {
+      const uint4 b = *reinterpret_cast<const uint4*>(x[m] + x_at + q * 64);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mma_bf16(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
+        mma_bf16(part[m][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
+      }
     }
   }
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc.v[h][c] = fmaf(part[h][c], ref[2 * h + (c >> 1)], acc.v[h][c]);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        acc[m].v[h][c] = fmaf(part[m][h][c], ref[2 * h + (c >> 1)], acc[m].v[h][c]);
 }
 
 // A lane's sums of a whole unit -> Y, at the lane's first output and row.
@@ -344,43 +367,38 @@ __device__ __forceinline__ uint32_t stage_scales(const Stage* st) {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 8;                 // of a slot
+constexpr int kRows = 8;                 // of an MMA; a slot holds MT times as many
 constexpr int kRing = 3;                 // steps of weight per warp: two in flight beside the one in use
 constexpr int kMaxUnits = 64;            // of a phase
-constexpr int kRedRow = kRows + 1;       // floats of an output's sums: one more against bank conflicts
-constexpr int kPart = kUnitRows * kRedRow;
 constexpr int kMaxSmem = 226 * 1024;     // 227 KB less the static part
 
-// Shared memory: rings; the warps' partial sums of their first and last unit; activations
+// Shared memory: rings; a warp's sums of a unit that an earlier warp began; activations
 // [row][step], pitch 64 bytes over the steps' 256 (rows on other banks); their scalings; the
 // CTA's sums for the cluster; the experts' slots and offsets.
 struct Layout {
-  int steps, rows, out_units, E;
+  int steps, rows, out_units, E, mt;
   static constexpr int kRingBytes = int(sizeof(Stage)) * kRing * kWarps;
-  static constexpr int kX = kRingBytes + kWarps * 2 * kPart * 4;
+  __host__ __device__ int x() const { return kRingBytes + kWarps * int(sizeof(Acc)) * 32 * mt; }
   __host__ __device__ int pitch() const { return steps * (kStepK * 2) + 64; }
-  __host__ __device__ int undo() const { return kX + rows * pitch(); }
-  __host__ __device__ int out() const { return undo() + steps * kRows * 4; }
+  __host__ __device__ int undo() const { return x() + rows * pitch(); }
+  __host__ __device__ int out() const { return undo() + steps * kRows * mt * 4; }
   __host__ __device__ int table() const { return out() + out_units * rows * kUnitRows * 4; }
   __host__ __device__ long long bytes() const { return (long long)table() + (E > 0 ? (E + 1) * 8 : 0); }
 };
 
-template <bool BF16, int VIEW>
+template <int MT, bool BF16, int VIEW>
 __global__ void __launch_bounds__(kThreads, 1)
 stream_kernel(const MatvecParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_span[kMaxUnits];  // warps that share a unit: first | last << 8 | (first one's which) << 16
+  constexpr int R = MT * kRows;  // rows of a slot
   const int all_steps = p.K / kStepK, S = p.splits;
   const int rank = S > 1 ? int(blockIdx.x) % S : 0;
   const int cluster = S > 1 ? int(blockIdx.x) / S : int(blockIdx.x);
   const int clusters = S > 1 ? int(gridDim.x) / S : int(gridDim.x);
   const int s_begin = all_steps * rank / S, steps = all_steps * (rank + 1) / S - s_begin;
-  const Layout lay{(all_steps + S - 1) / S, p.x_rows, p.out_units, p.E};
-  // a warp's sums of its share's first unit (which 0) or last (1)
-  auto part_of = [&](int w, int which) {
-    return reinterpret_cast<float*>(smem + Layout::kRingBytes) + (w * 2 + which) * kPart;
-  };
-  uint8_t* const s_x = smem + Layout::kX;
+  const Layout lay{(all_steps + S - 1) / S, p.x_rows, p.out_units, p.E, MT};
+  Acc* const s_part = reinterpret_cast<Acc*>(smem + Layout::kRingBytes);  // [warp][half][lane]
+  uint8_t* const s_x = smem + lay.x();
   float* const s_undo = reinterpret_cast<float*>(smem + lay.undo());
   float* const s_out = reinterpret_cast<float*>(smem + lay.out());  // [unit][row][32]
   int* const s_table = reinterpret_cast<int*>(smem + lay.table());  // [E + 1] slots before each expert
@@ -402,7 +420,7 @@ stream_kernel(const MatvecParams p) {
       for (int base = 0; base < p.E; base += 32) {
         const int e = base + lane;
         const int rows = e < p.E ? s_offsets[e + 1] - s_offsets[e] : 0;
-        int incl = (rows + kRows - 1) / kRows;
+        int incl = (rows + R - 1) / R;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
@@ -515,7 +533,7 @@ stream_kernel(const MatvecParams p) {
           bool wide;
           v[b] = scale_bf16(v[b], &undo, &wide);
           if (c == 0 && at[b] >= 0) {
-            s_undo[ss * kRows + rr] = undo;
+            s_undo[ss * R + rr] = undo;
             any_wide |= wide;
           }
         }
@@ -537,7 +555,7 @@ stream_kernel(const MatvecParams p) {
       slot = now;
       e = expert_of(slot);
       const int row_first = p.E > 0 ? s_offsets[e] : 0, row_last = p.E > 0 ? s_offsets[e + 1] : p.M;
-      row0 = row_first + (slot - (p.E > 0 ? s_table[e] : 0)) * kRows;
+      row0 = row_first + (slot - (p.E > 0 ? s_table[e] : 0)) * R;
       rows = max(1, min(min(row_last, p.M) - row0, p.x_rows));
       scale = p.w_scale[size_t(e) * 4];
       wide = __syncthreads_or(stage_x(row0, rows, BF16)) != 0;
@@ -547,105 +565,105 @@ stream_kernel(const MatvecParams p) {
       }
     }
 
+    // The warps share the list of the phase's (unit, step) evenly. The warp that has a unit's
+    // first step owns its sums: it adds those of the warps behind it in their order.
     const unsigned n = unsigned(end - at) * unsigned(steps);
-    if (int(threadIdx.x) < end - at) {
-      // the warp that holds step i of the list is the last w with n * w / 16 <= i
-      const unsigned lo = threadIdx.x * unsigned(steps);
-      const unsigned w0 = ((lo + 1) * kWarps - 1) / n, w1 = ((lo + steps) * kWarps - 1) / n;
-      s_span[threadIdx.x] = int(w0 | w1 << 8 | (n * w0 / kWarps == lo ? 0u : 1u) << 16);
-    }
     // a row past the last reads the first one's: its sums are never stored
-    const uint8_t* const x_row = s_x + (g < rows ? g : 0) * lay.pitch() + t * 16;
+    const uint8_t* x_row[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) x_row[m] = s_x + (m * kRows + g < rows ? m * kRows + g : 0) * lay.pitch() + t * 16;
     const int i_begin = int(n * warp / kWarps), i_end = int(n * (warp + 1) / kWarps);
-    int unit = i_begin / steps;
-    for (int i = i_begin, which = 0; i < i_end; ++unit, which = 1) {
-      const int seg_end = min(i_end, (unit + 1) * steps);
-      const bool whole = i == unit * steps && seg_end == (unit + 1) * steps;
-      Acc acc;
+    int unit = i_begin / steps, unit_end = (unit + 1) * steps;
+    auto finish = [&](const Acc (&acc)[MT]) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int m = 0; m < MT; ++m) {
+        const int row = m * kRows + 2 * t;
+        if (S > 1) {
+          float* out = s_out + (unit * rows + row) * kUnitRows + g;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc.v[h][c] = 0.f;
-      auto run = [&](auto as_bf16) {
-        for (int s = i - unit * steps; i < seg_end; ++i, ++s) {
-          copies_wait<kRing - 2>();
-          __syncwarp();  // the scale words come from four lanes; the stage before has been read
-          fetch(pos == 0 ? kRing - 1 : pos - 1);
-          const uint8_t* x = x_row + s * (kStepK * 2);
-          if constexpr (decltype(as_bf16)::value)
-            step_bf16<VIEW>(acc, ring[pos], x);
+          for (int j = 0; j < 2; ++j)
+            if (j < rows - row) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) out[j * kUnitRows + i * 8] = acc[m].v[i >> 1][(i & 1) * 2 + j];
+            }
+        } else {
+          const size_t y = size_t(row0 + row) * p.ldy + output_of(base + unit, g);
+          if (p.y_dtype == SHARQ_BF16)
+            store_unit<SHARQ_BF16>(p, acc[m], y, rows - row, scale);
+          else if (p.y_dtype == SHARQ_F16)
+            store_unit<SHARQ_F16>(p, acc[m], y, rows - row, scale);
           else
-            step_f16<VIEW, BF16>(acc, ring[pos], x, s_undo + s * kRows + 2 * t);
-          pos = pos + 1 == kRing ? 0 : pos + 1;
+            store_unit<SHARQ_F32>(p, acc[m], y, rows - row, scale);
         }
-      };
-      if constexpr (BF16) {
-        if (wide) run(std::true_type()); else run(std::false_type());
-      } else {
-        run(std::false_type());
       }
-      if (!whole) {
-        float* part = part_of(warp, which) + g * kRedRow + 2 * t;
+    };
+    Acc acc[MT];
+    bool open = false;  // acc: a unit of this warp's that others have steps of
+    for (int i = i_begin; i < i_end;) {
+      const bool own = i + steps == unit_end;
+      const int seg_end = min(i_end, unit_end);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            part[(2 * h + (c >> 1)) * 8 * kRedRow + (c & 1)] = acc.v[h][c];
-      } else if (S > 1) {
-        float* out = s_out + (unit * rows + 2 * t) * kUnitRows + g;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (j < rows - 2 * t) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) out[j * kUnitRows + i * 8] = acc.v[i >> 1][(i & 1) * 2 + j];
-          }
-      } else {
-        const size_t y = size_t(row0 + 2 * t) * p.ldy + output_of(base + unit, g);
-        if (p.y_dtype == SHARQ_BF16)
-          store_unit<SHARQ_BF16>(p, acc, y, rows - 2 * t, scale);
-        else if (p.y_dtype == SHARQ_F16)
-          store_unit<SHARQ_F16>(p, acc, y, rows - 2 * t, scale);
+      for (int j = 0; j < MT * 8; ++j) acc[j >> 3].v[(j >> 2) & 1][j & 3] = 0.f;
+      for (int s = i - (unit_end - steps); i < seg_end; ++i, ++s) {
+        copies_wait<kRing - 2>();
+        __syncwarp();  // the scale words come from four lanes; the stage before has been read
+        fetch(pos == 0 ? kRing - 1 : pos - 1);
+        const int x_at = s * (kStepK * 2);
+        if (BF16 && wide)
+          step_bf16<MT, VIEW>(acc, ring[pos], x_row, x_at);
         else
-          store_unit<SHARQ_F32>(p, acc, y, rows - 2 * t, scale);
+          step_f16<MT, VIEW, BF16>(acc, ring[pos], x_row, x_at, s_undo + s * R + 2 * t);
+        pos = pos + 1 == kRing ? 0 : pos + 1;
       }
+      if (!own) {
+        float4* part = reinterpret_cast<float4*>(s_part + warp * MT * 32) + lane;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            part[(m * 2 + h) * 32] = make_float4(acc[m].v[h][0], acc[m].v[h][1], acc[m].v[h][2], acc[m].v[h][3]);
+      } else if (seg_end == unit_end) {
+        finish(acc);
+      } else {
+        open = true;
+        break;
+      }
+      ++unit;
+      unit_end += steps;
     }
     __syncthreads();
-
-    // units that several warps share, in the warps' order: a warp takes 32 outputs of a row
-    const int nu = end - at;
-    int u = warp, m = 0;
-    while (u >= nu && m < rows) { u -= nu; ++m; }
-    while (m < rows) {
-      const int span = s_span[u], w0 = span & 255, w1 = (span >> 8) & 255;
-      if (w0 != w1) {
-        float v = part_of(w0, span >> 16)[lane * kRedRow + m];
-        constexpr int kNext = 2 * kPart;
-        const float* next = part_of(w0 + 1, 0) + lane * kRedRow + m;
-        if (n >= unsigned(kWarps)) {
-          for (int w = w1 - w0; w > 0; w -= 4, next += 4 * kNext) {
-            const float x0 = next[0], x1 = w > 1 ? next[kNext] : 0.f, x2 = w > 2 ? next[2 * kNext] : 0.f,
-                        x3 = w > 3 ? next[3 * kNext] : 0.f;
-            v += x0;
-            v += x1;
-            v += x2;
-            v += x3;
-          }
-        } else {  // fewer steps than warps: some shares are empty
-          for (int w = w0 + 1; w <= w1; ++w, next += kNext)
-            if (n * unsigned(w) / kWarps < n * unsigned(w + 1) / kWarps) v += *next;
+    if (open) {
+      // the other shares in the unit are [warp + 1, behind); four at a time are asked for together
+      const int behind = min(int((unsigned(unit_end) * kWarps - 1) / n) + 1, kWarps);
+#pragma unroll 1
+      for (int w = warp + 1; w < behind; w += 4) {
+        float4 v[4][2 * MT];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4* part = reinterpret_cast<const float4*>(s_part + min(w + j, kWarps - 1) * MT * 32) + lane;
+#pragma unroll
+          for (int h = 0; h < 2 * MT; ++h) v[j][h] = part[h * 32];
         }
-        if (S > 1)
-          s_out[(u * rows + m) * kUnitRows + lane] = v;
-        else
-          store_y(p, size_t(row0 + m) * p.ldy + output_of(base + u, lane), v * scale);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // with fewer steps than warps some have no share
+          if (w + j >= behind || (n < unsigned(kWarps) && n * (w + j) / kWarps == n * (w + j + 1) / kWarps)) continue;
+#pragma unroll
+          for (int h = 0; h < 2 * MT; ++h) {
+            float* to = acc[h >> 1].v[h & 1];
+            to[0] += v[j][h].x;
+            to[1] += v[j][h].y;
+            to[2] += v[j][h].z;
+            to[3] += v[j][h].w;
+          }
+        }
       }
-      u += kWarps;
-      while (u >= nu && m < rows) { u -= nu; ++m; }
+      finish(acc);
     }
     if (S > 1) {
       ptx::cluster_sync();
       int cu = 0, cm = rank * kWarps + warp;
-      for (int i = cm; i < nu * rows; i += S * kWarps, cm += S * kWarps) {
+      for (int i = cm; i < (end - at) * rows; i += S * kWarps, cm += S * kWarps) {
         while (cm >= rows) { cm -= rows; ++cu; }
         const uint32_t a = ptx::smem_u32(s_out + i * kUnitRows + lane);
         float v[8];
@@ -672,9 +690,9 @@ stream_kernel(const MatvecParams p) {
 
 // K over as few CTAs as let the activations fit, beside the sums of at least two units; 0 where
 // not even eight do.
-int splits_for(int steps, int rows, int E) {
+int splits_for(int steps, int rows, int E, int mt) {
   for (int S = 1; S <= 8 && S <= steps; S *= 2)
-    if (steps / S < 4096 && Layout{(steps + S - 1) / S, rows, S > 1 ? 2 : 0, E}.bytes() <= kMaxSmem) return S;
+    if (steps / S < 4096 && Layout{(steps + S - 1) / S, rows, S > 1 ? 2 : 0, E, mt}.bytes() <= kMaxSmem) return S;
   return 0;
 }
 
@@ -710,16 +728,16 @@ cudaError_t max_clusters(Kernel* kern, int S, int num_sms, unsigned long long ct
   return cudaSuccess;
 }
 
-template <bool BF16, int VIEW>
+template <int MT, bool BF16, int VIEW>
 cudaError_t launch_stream(MatvecParams p, int num_sms, unsigned long long ctx, cudaStream_t st) {
   const int steps = p.K / kStepK;
-  p.x_rows = p.E > 0 ? kRows : p.M;
-  p.splits = splits_for(steps, p.x_rows, p.E);
+  p.x_rows = p.E > 0 ? MT * kRows : p.M;
+  p.splits = splits_for(steps, p.x_rows, p.E, MT);
   p.out_units = 0;
   if (p.splits == 0) return cudaErrorInvalidConfiguration;
-  Layout lay{(steps + p.splits - 1) / p.splits, p.x_rows, 0, p.E};
+  Layout lay{(steps + p.splits - 1) / p.splits, p.x_rows, 0, p.E, MT};
   int clusters = num_sms;
-  auto* kern = stream_kernel<BF16, VIEW>;
+  auto* kern = stream_kernel<MT, BF16, VIEW>;
   static std::atomic<unsigned long long> done{~0ull};
   cudaError_t e = allow_smem(kern, kMaxSmem, ctx, &done);
   if (e != cudaSuccess) return e;
@@ -748,23 +766,38 @@ cudaError_t launch_stream(MatvecParams p, int num_sms, unsigned long long ctx, c
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// MMAs of eight rows that a slot takes, 0 where the tiles take the call. Measured, this kernel
+// against the tiles, us: one weight of 4096 x 28672, bf16, 8 rows 17 / 29, 9 rows 22 / 29, 16 rows
+// 26 / 29 (fp16 15 / 23, 19 / 23, 24 / 23); 14336 x 4096, 9 rows 15.2 / 17.5, 16 rows 16.4 / 17.7;
+// 4096 x 4096, 9 rows 9.5 / 8.9, 16 rows 9.7 / 9.2 (fp16 7.3 / 8.2, 7.9 / 8.4). Experts, whose
+// slots are seldom full, fp16: 8 of 14336 x 4096, 8 rows each on average 72 / 81, 12 rows 111 / 83
+// (two MMAs a slot; one: 103); 8 of 4096 x 28672, 8 rows 117 / 142, 12 rows 177 / 133.
+int row_tiles(int M, int E, int K) {
+  const int mt = (E > 0 ? M <= kRows * E : M <= kRows) ? 1 : E == 0 && M <= 2 * kRows ? 2 : 0;
+  return mt > 0 && splits_for(K / kStepK, E > 0 ? kRows : M, E, mt) > 0 ? mt : 0;
+}
+
+template <int MT>
+cudaError_t launch_rows_of(const MatvecParams& p, bool bf16, ScaleView view, int num_sms,
+                           unsigned long long ctx, cudaStream_t st) {
+  switch (view) {
+    case kE4M3x16:
+      return bf16 ? launch_stream<MT, true, kE4M3x16>(p, num_sms, ctx, st) : launch_stream<MT, false, kE4M3x16>(p, num_sms, ctx, st);
+    case kE4M3x32:
+      return bf16 ? launch_stream<MT, true, kE4M3x32>(p, num_sms, ctx, st) : launch_stream<MT, false, kE4M3x32>(p, num_sms, ctx, st);
+    default:
+      return bf16 ? launch_stream<MT, true, kE8M0x32>(p, num_sms, ctx, st) : launch_stream<MT, false, kE8M0x32>(p, num_sms, ctx, st);
+  }
+}
+
 }  // namespace
 
-bool matvec_streams(int M, int E, int K) {
-  if (E > 0 ? M > kRows * E : M > kRows) return false;
-  return splits_for(K / kStepK, E > 0 ? kRows : M, E) > 0;
-}
+bool matvec_streams(int M, int E, int K) { return row_tiles(M, E, K) > 0; }
 
 cudaError_t launch_matvec(const MatvecParams& p, bool bf16, ScaleView view, int num_sms,
                           unsigned long long ctx, cudaStream_t st) {
-  switch (view) {
-    case kE4M3x16:
-      return bf16 ? launch_stream<true, kE4M3x16>(p, num_sms, ctx, st) : launch_stream<false, kE4M3x16>(p, num_sms, ctx, st);
-    case kE4M3x32:
-      return bf16 ? launch_stream<true, kE4M3x32>(p, num_sms, ctx, st) : launch_stream<false, kE4M3x32>(p, num_sms, ctx, st);
-    default:
-      return bf16 ? launch_stream<true, kE8M0x32>(p, num_sms, ctx, st) : launch_stream<false, kE8M0x32>(p, num_sms, ctx, st);
-  }
+  return row_tiles(p.M, p.E, p.K) == 2 ? launch_rows_of<2>(p, bf16, view, num_sms, ctx, st)
+                                       : launch_rows_of<1>(p, bf16, view, num_sms, ctx, st);
 }
 
 }  // namespace sharq

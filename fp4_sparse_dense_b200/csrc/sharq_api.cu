@@ -845,7 +845,6 @@ sharq_status sharq_sort_tokens(const void* experts, int32_t id_bits, const sharq
   p.experts = experts;
   p.ids64 = id_bits == 64;
   p.n = t->T * t->k;
-  p.k = t->k;
   p.E = t->E;
   p.offsets = t->offsets;
   p.order = t->order;

@@ -275,7 +275,11 @@ SHARQ_API sharq_status sharq_linear_noalloc(const sharq_act* act, const sharq_we
  * configuration; pair masks are read through scales_sparse, the others through scales_dense.
  * Y: device [M][N], F16, BF16 or F32. Infinite and NaN activations reach the outputs of
  * their own row as in a float32 product. The weight is read once per 32 rows: for many rows
- * sharq_prepare + sharq_linear is the faster path. M <= 2^21 (else SHARQ_ERR_UNSUPPORTED). */
+ * sharq_prepare + sharq_linear is the faster path. Y overlaps neither X nor w.
+ * M <= 2^21 (else SHARQ_ERR_UNSUPPORTED).
+ * Ordering: as sharq_linear's; here the weight may be loaded early at every M. Calls with more
+ * than 16 rows (or too long a K for fewer) use tensor memory and bounded waits; a wait that runs
+ * out is reported by sharq_read_device_status, and Y is then incomplete. */
 SHARQ_API sharq_status sharq_matvec(const void* X, size_t ldx, int32_t M, sharq_dtype dtype,
                                     const sharq_weight* w, void* Y, size_t ldy,
                                     sharq_dtype y_dtype, void* stream);
@@ -324,7 +328,9 @@ SHARQ_API sharq_status sharq_sort_tokens_backward(const void* d_rows, size_t ld_
 /* Y[p] = X row of sorted row p * deq(W of its expert), as sharq_matvec, for p < offsets[E];
  * rows behind that are left as they were. gather == 0: X holds the sorted rows [T * k][K];
  * gather == 1: X holds the tokens [T][K] and row p reads token order[p] / k. tokens->E must
- * equal w->E. */
+ * equal w->E. The number of rows is known on the device only, so nothing of the weight is loaded
+ * before the kernel launched just before this call has completed. T * k <= 2^19 and E * N < 2^31
+ * (else SHARQ_ERR_UNSUPPORTED). */
 SHARQ_API sharq_status sharq_expert_matvec(const void* X, size_t ldx, int32_t gather,
                                            sharq_dtype dtype, const sharq_tokens* tokens,
                                            const sharq_expert_weights* w, void* Y, size_t ldy,
