@@ -126,6 +126,13 @@ def test_expert_matvec_refuses(sq):  # noqa: F811
     assert f(P, 256, 0, BF16, many, w, P, 128, BF16, None) == UNSUPPORTED
 
 
+def test_expert_matvec_refuses_outputs_beyond_32_bits(sq):  # noqa: F811
+    """The copies' coordinate counts the outputs of all experts."""
+    t, n = ctypes.byref(tokens(sq, E=1024)), 1 << 21
+    w = ctypes.byref(experts(sq, E=1024, N=n))
+    assert sq.sharq_expert_matvec(P, 256, 0, BF16, t, w, P, n, BF16, None) == UNSUPPORTED
+
+
 # ------------------------------------------------------------------ the tensor-level helpers
 
 def test_cpu_tensors_are_refused(sq):  # noqa: F811
