@@ -108,6 +108,14 @@ def _readable(name, x, align16=False):
     return x.clone(memory_format=torch.contiguous_format), rows, cols, cols
 
 
+def _new(like, rows, cols, dtype=None):
+    """An empty matrix on the device of `like`, in its dtype by default (new_empty takes half a
+    microsecond less than torch.empty with a device)."""
+    if dtype is None:
+        return like.new_empty((rows, cols))
+    return like.new_empty((rows, cols), dtype=dtype)
+
+
 # ------------------------------------------------------------------ the few-row product
 
 def matvec(X, w: QuantWeight, out=None, out_dtype=None, stream=None):
@@ -131,7 +139,7 @@ def matvec(X, w: QuantWeight, out=None, out_dtype=None, stream=None):
     if w.codes.device != device:
         raise ValueError(f"w is on {w.codes.device}, expected {device}")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or X.dtype, device=device)
+        out = _new(X, M, N, out_dtype)
         ldy = N
     else:
         ldy = _matrix("out", out, M, N, device)
@@ -236,11 +244,11 @@ class SortedTokens(_CStructCache):
                             self.T, self.k, self.E)
 
 
-def _empty_tokens(T, k, E, device) -> SortedTokens:
+def _empty_tokens(T, k, E, like) -> SortedTokens:
     """SortedTokens over one new buffer; its parts fit by construction, so the C struct is made
     here without the checks of _make_c."""
     n = T * k
-    plan = torch.empty(2 * n + E + 1, dtype=torch.int32, device=device)
+    plan = like.new_empty(2 * n + E + 1, dtype=torch.int32)
     order, place, offsets = plan.split_with_sizes((n, n, E + 1))
     t = object.__new__(SortedTokens)
     p = plan.data_ptr()
@@ -272,7 +280,7 @@ def sort_tokens(experts, num_experts: int, X=None, rows=None, out: SortedTokens 
     if not experts.is_contiguous():
         experts = experts.contiguous()
     if out is None:
-        out = _empty_tokens(T, k, num_experts, device)
+        out = _empty_tokens(T, k, num_experts, experts)
     elif (out.T, out.k, out.E) != (T, k, num_experts):
         raise ValueError(f"out is for T, k, E = {out.T}, {out.k}, {out.E}")
     else:
@@ -286,7 +294,7 @@ def sort_tokens(experts, num_experts: int, X=None, rows=None, out: SortedTokens 
             raise ValueError(f"X must be [{T}, H], got {list(X.shape)}")
         code = _code("X", X)
         if rows is None:
-            rows = torch.empty((T * k, H), dtype=X.dtype, device=device)
+            rows = _new(X, T * k, H)
             ld_rows = H
         else:
             ld_rows = _matrix("rows", rows, T * k, H, device)
@@ -326,7 +334,7 @@ def expert_matvec(X, w: ExpertWeights, tokens: SortedTokens, gather: bool = Fals
     if w.codes.device != device or tokens.offsets.device != device:
         raise ValueError(f"w is on {w.codes.device}, tokens on {tokens.offsets.device}, expected {device}")
     if out is None:
-        out = torch.empty((n, w.N), dtype=out_dtype or X.dtype, device=device)
+        out = _new(X, n, w.N, out_dtype)
         ldy = w.N
     else:
         ldy = _matrix("out", out, n, w.N, device)
@@ -365,7 +373,7 @@ def combine_tokens(rows, tokens: SortedTokens, weights=None, out=None, stream=No
     if weights is not None:
         weights = _weights(weights, tokens, device)
     if out is None:
-        out = torch.empty((tokens.T, H), dtype=rows.dtype, device=device)
+        out = _new(rows, tokens.T, H)
         ldy = H
     else:
         ldy = _matrix("out", out, tokens.T, H, device)
@@ -400,14 +408,14 @@ def combine_tokens_backward(dY, rows, tokens: SortedTokens, weights, d_rows=None
         raise ValueError(f"tokens on {tokens.offsets.device}, expected {device}")
     weights = _weights(weights, tokens, device)
     if d_rows is None:
-        d_rows = torch.empty((T * k, H), dtype=rows.dtype, device=device)
+        d_rows = _new(rows, T * k, H)
         ld_d = H
     else:
         ld_d = _matrix("d_rows", d_rows, T * k, H, device)
         if d_rows.dtype != rows.dtype:
             raise TypeError(f"d_rows is {d_rows.dtype}, rows is {rows.dtype}")
     if d_weights is None:
-        d_weights = torch.empty((T, k), dtype=torch.float32, device=device)
+        d_weights = _new(weights, T, k)
     elif d_weights.dtype != torch.float32 or list(d_weights.shape) != [T, k] or not d_weights.is_contiguous():
         raise ValueError(f"d_weights must be contiguous float32 [{T}, {k}]")
     else:
