@@ -143,7 +143,7 @@ struct Acc {
 // One step with f16 operands. x: the lane's row at its K unit 4 t of the step, unit 4 t + q 64 q
 // bytes on; undo: what takes the scaling of rows 2 t and 2 t + 1 out.
 template <int MT, int VIEW, bool SCALED>
-__device__ __forceinline__ void step_f16(Acc (&acc)[MT], const Stage& st, const uint8_t* const (&x)[MT], int x_at,
+__device__ __forceinline__ void step_f16(Acc (&acc)[MT], const Stage& st, const uint8_t* const (&x)[MT],
                                          const float* undo) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t pick = uint32_t(t) | uint32_t(4 + t) << 4;  // byte t of two words
@@ -220,7 +220,7 @@ __device__ __forceinline__ void step_f16(Acc (&acc)[MT], const Stage& st, const 
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const uint4 b = *reinterpret_cast<const uint4*>(x[m] + x_at + q * 64);
+        const uint4 b = *reinterpret_cast<const uint4*>(x[m] + q * 64);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (q == 0)
@@ -254,7 +254,7 @@ __device__ __forceinline__ void step_f16(Acc (&acc)[MT], const Stage& st, const 
 // (E4M3: sf * 2^118, finite up to 448; E8M0: 2^(126 + b - b_max)), the rest with the sum.
 // The codes go in step_f16's order, so that both kinds of operands give the same bits.
 template <int MT, int VIEW>
-__device__ __forceinline__ void step_bf16(Acc (&acc)[MT], const Stage& st, const uint8_t* const (&x)[MT], int x_at) {
+__device__ __forceinline__ void step_bf16(Acc (&acc)[MT], const Stage& st, const uint8_t* const (&x)[MT]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint4 sv = st.scales[VIEW == kE4M3x16 ? t >> 1 : 0][g];
   const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
@@ -300,7 +300,7 @@ __device__ __forceinline__ void step_bf16(Acc (&acc)[MT], const Stage& st, const
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const uint4 b = *reinterpret_cast<const uint4*>(x[m] + x_at + q * 64);
+      const uint4 b = *reinterpret_cast<const uint4*>(x[m] + q * 64);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         mma_bf16(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
@@ -608,11 +608,13 @@ stream_kernel(const MatvecParams p) {
         copies_wait<kRing - 2>();
         __syncwarp();  // the scale words come from four lanes; the stage before has been read
         fetch(pos == 0 ? kRing - 1 : pos - 1);
-        const int x_at = s * (kStepK * 2);
+        const uint8_t* x[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) x[m] = x_row[m] + s * (kStepK * 2);
         if (BF16 && wide)
-          step_bf16<MT, VIEW>(acc, ring[pos], x_row, x_at);
+          step_bf16<MT, VIEW>(acc, ring[pos], x);
         else
-          step_f16<MT, VIEW, BF16>(acc, ring[pos], x_row, x_at, s_undo + s * R + 2 * t);
+          step_f16<MT, VIEW, BF16>(acc, ring[pos], x, s_undo + s * R + 2 * t);
         pos = pos + 1 == kRing ? 0 : pos + 1;
       }
       if (!own) {
