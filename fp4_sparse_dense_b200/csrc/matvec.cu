@@ -27,7 +27,7 @@
 // (matvec_tile.cu).
 //
 // Measured (B200, weights cycling through more than L2 or nearly so; N x K/2 codes and scales
-// over time): 4096 x 28672 NVFP4 / 16, 1 row 14.8 us (4.5 TB/s); 14336 x 4096, 8 rows 13.5 us
+// over time): 4096 x 28672 NVFP4 / 16, 1 row 14.5 us (4.6 TB/s); 14336 x 4096, 8 rows 13.6 us
 // (2.3 TB/s); 4096 x 4096, 1 row 5.3 us (1.7 TB/s). The loop runs near memory rate; what remains
 // is the start (launch, activations, the first weights: about 3 us) and the sums and stores
 // (about 1 us), which a short weight cannot hide. The code that runs once per launch comes cold
