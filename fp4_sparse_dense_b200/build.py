@@ -54,7 +54,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     tmp = LIB + ".tmp"
     base = [nvcc(), *NVCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include")]
     # the sources do not depend on one another: one nvcc each, a link at the end
-    with tempfile.TemporaryDirectory() as objects, ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+    with tempfile.TemporaryDirectory(dir=LIB_DIR) as objects, ThreadPoolExecutor(os.cpu_count() or 1) as pool:
         objs = [os.path.join(objects, f[:-3] + ".o") for f in SOURCES]
         cmds = [[*base, "-c", "-o", o, os.path.join(CSRC, f)] for f, o in zip(SOURCES, objs)]
         link = [*base, "-shared", "-cudart", "static", "-o", tmp, *objs]
