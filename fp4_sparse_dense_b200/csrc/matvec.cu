@@ -40,8 +40,8 @@
 // - E4M3 scales: e2m1 * sf has at most 6 significant bits between 2^-10 and 2688: exact.
 // - E8M0 scales: relative to the row's first scale of the step, 2^(b - b_0), exact within
 //   2^-14 ... 2^13; the step's sum is multiplied by 2^(b_0 - 127) when it joins the
-//   accumulator. A wider spread takes passes over the step's codes, relative to the largest
-//   scale and 24 binades each.
+//   accumulator. Otherwise relative to the row's largest scale, within 2^-23 ... 1, where blocks
+//   of zeros (their scale byte is 0) do not count. A wider spread takes a pass per block of 32 K.
 // - fp16 activations enter as they are. bf16 ones are scaled by a power of two per (row,
 //   step) so that the largest one's exponent is 15; exact for 32 binades, and the scale is
 //   taken out with the step's sum. Where some (row, step) of a CTA has a wider spread, or
@@ -140,96 +140,42 @@ struct Acc {
   float v[2][4];  // (h, c): output 32 (2 h + c / 2) + g of the lane's quarter, row 2 t + c % 2
 };
 
-// One step with f16 operands. x: the lane's row at its K unit 4 t of the step, unit 4 t + q 64 q
-// bytes on; undo: what takes the scaling of rows 2 t and 2 t + 1 out.
-template <int MT, int VIEW, bool SCALED>
-__device__ __forceinline__ void step_f16(Acc (&acc)[MT], const Stage& st, const uint8_t* const (&x)[MT],
-                                         const float* undo) {
+// A step whose E8M0 scales lie too far apart for one f16 operand, block by block of 32 K. Lane t
+// holds block t of both operands, so the other lanes' are zeroed in its pass (a zero of one never
+// meets an infinity of the other), and the pass's sums are multiplied by their output's own scale.
+// 14336 x 4096, 8 fp16 rows, every second block 2^-30 of its neighbours: 26.0 us (ordinary scales
+// 12.3; a block of zeros per output, which does not get here, 13.0).
+template <int MT, bool SCALED>
+__device__ __forceinline__ void step_f16_apart(Acc (&acc)[MT], const Stage& st,
+                                               const uint8_t* const (&x)[MT], const float* undo) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t pick = uint32_t(t) | uint32_t(4 + t) << 4;  // byte t of two words
-  const uint4 sv = st.scales[VIEW == kE4M3x16 ? t >> 1 : 0][g];
-  const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
-  int wp = 0, wpasses = 1;
-  bool narrow = true;
-  if (VIEW == kE8M0x32) {
-    uint32_t off = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int d = int((sw[i] >> (8 * t)) & 0xFFu) - int(sw[i] & 0xFFu);
-      off |= uint32_t(d + 14) > 27u || ((sw[i] & 0xFFu) - 1u) > 189u;
-    }
-    narrow = __all_sync(0xFFFFFFFFu, off == 0);
-    if (!narrow) {
-      int spread = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b0 = sw[i] & 0xFFu, b1 = (sw[i] >> 8) & 0xFFu, b2 = (sw[i] >> 16) & 0xFFu,
-                  b3 = sw[i] >> 24;
-        spread = max(spread, max(max(b0, b1), max(b2, b3)) - min(min(b0, b1), min(b2, b3)));
-      }
-      wpasses = __reduce_max_sync(0xFFFFFFFFu, spread) / 24 + 1;
-    }
-  }
-  do {
-    uint32_t f[4][2];
-    float ref[4];  // power of two that the row's factors leave out
-    if (VIEW == kE4M3x16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t two = e4m3x2_f16x2(sw[i] >> ((t & 1) * 16));
-        f[i][0] = __byte_perm(two, two, 0x1010);
-        f[i][1] = __byte_perm(two, two, 0x3232);
-      }
-    } else if (VIEW == kE4M3x32) {
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const uint32_t two = e4m3x2_f16x2(__byte_perm(sw[i], sw[i + 1], pick));
-        f[i][0] = f[i][1] = __byte_perm(two, two, 0x1010);
-        f[i + 1][0] = f[i + 1][1] = __byte_perm(two, two, 0x3232);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = int((sw[i] >> (8 * t)) & 0xFFu);
-        int r;
-        if (narrow) {
-          r = int(sw[i] & 0xFFu);
-          f[i][0] = uint32_t(b - r + 15) * 0x04000400u;
-        } else {
-          const int b0 = sw[i] & 0xFFu, b1 = (sw[i] >> 8) & 0xFFu, b2 = (sw[i] >> 16) & 0xFFu,
-                    b3 = sw[i] >> 24;
-          const int top = max(max(b0, b1), max(b2, b3)) - 24 * wp;  // this pass: (top - 24, top]
-          r = max(top, 1);
-          f[i][0] = b <= top && b > top - 24 ? f16_pow2(b - r) : 0u;
-        }
-        ref[i] = __uint_as_float(uint32_t(r) << 23);
-        f[i][1] = f[i][0];
-      }
-    }
+#pragma unroll 1
+  for (int block = 0; block < 4; ++block) {
+    const uint32_t keep = t == block ? 0xFFFFFFFFu : 0u;
     float part[MT][2][4];
-    const uint4 cw[4] = {st.codes[0][lane], st.codes[1][lane], st.codes[2][lane], st.codes[3][lane]};
+#pragma unroll
+    for (int i = 0; i < MT * 8; ++i) part[i >> 3][(i >> 2) & 1][i & 3] = 0.f;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint32_t a[4][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w = q == 0 ? cw[i].x : q == 1 ? cw[i].y : q == 2 ? cw[i].z : cw[i].w;
-        widen(w, a[i]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[i][j] = mul_f16x2(a[i][j], f[i][q >> 1]);
-      }
+      for (int i = 0; i < 4; ++i) widen(reinterpret_cast<const uint32_t*>(&st.codes[i][lane])[q] & keep, a[i]);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const uint4 b = *reinterpret_cast<const uint4*>(x[m] + q * 64);
+        uint4 b = *reinterpret_cast<const uint4*>(x[m] + q * 64);
+        b = make_uint4(b.x & keep, b.y & keep, b.z & keep, b.w & keep);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (q == 0)
-            mma_f16_first(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
-          else
-            mma_f16(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
+          mma_f16(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
           mma_f16(part[m][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
         }
       }
+    }
+    float ref[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t e = (reinterpret_cast<const uint32_t*>(&st.scales[0][g])[i] >> (8 * block)) & 0xFFu;
+      ref[i] = __uint_as_float(e ? e << 23 : 1u << 22);
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -239,15 +185,123 @@ __device__ __forceinline__ void step_f16(Acc (&acc)[MT], const Stage& st, const 
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float v = part[m][h][c], o = c & 1 ? out.y : out.x;
-          float& to = acc[m].v[h][c];
-          if (VIEW == kE8M0x32)
-            to = fmaf(SCALED ? v * o : v, ref[2 * h + (c >> 1)], to);
-          else
-            to = SCALED ? fmaf(v, o, to) : to + v;
+          const float v = part[m][h][c];
+          acc[m].v[h][c] = fmaf(SCALED ? v * (c & 1 ? out.y : out.x) : v, ref[2 * h + (c >> 1)], acc[m].v[h][c]);
         }
     }
-  } while (VIEW == kE8M0x32 && ++wp < wpasses);
+  }
+}
+
+// One step with f16 operands. x: the lane's row at its K unit 4 t of the step, unit 4 t + q 64 q
+// bytes on; undo: what takes the scaling of rows 2 t and 2 t + 1 out.
+template <int MT, int VIEW, bool SCALED>
+__device__ __forceinline__ void step_f16(Acc (&acc)[MT], const Stage& st, const uint8_t* const (&x)[MT],
+                                         const float* undo) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const uint32_t pick = uint32_t(t) | uint32_t(4 + t) << 4;  // byte t of two words
+  const uint4 sv = st.scales[VIEW == kE4M3x16 ? t >> 1 : 0][g];
+  const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
+  uint32_t f[4][2];
+  float ref[4];  // power of two that the row's factors leave out
+  if (VIEW == kE4M3x16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t two = e4m3x2_f16x2(sw[i] >> ((t & 1) * 16));
+      f[i][0] = __byte_perm(two, two, 0x1010);
+      f[i][1] = __byte_perm(two, two, 0x3232);
+    }
+  } else if (VIEW == kE4M3x32) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const uint32_t two = e4m3x2_f16x2(__byte_perm(sw[i], sw[i + 1], pick));
+      f[i][0] = f[i][1] = __byte_perm(two, two, 0x1010);
+      f[i + 1][0] = f[i + 1][1] = __byte_perm(two, two, 0x3232);
+    }
+  } else {
+    uint32_t off = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = int((sw[i] >> (8 * t)) & 0xFFu) - int(sw[i] & 0xFFu);
+      off |= uint32_t(d + 14) > 27u || ((sw[i] & 0xFFu) - 1u) > 189u;
+    }
+    if (__all_sync(0xFFFFFFFFu, off == 0)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = int(sw[i] & 0xFFu);
+        f[i][0] = f[i][1] = uint32_t(int((sw[i] >> (8 * t)) & 0xFFu) - r + 15) * 0x04000400u;
+        ref[i] = __uint_as_float(uint32_t(r) << 23);
+      }
+    } else {
+      // Relative to the row's largest scale, up to 23 binades. A block of zeros does not count:
+      // its scale is the format's smallest, and whatever finite factor it gets it stays 0.
+      uint32_t top = 0, low = 0;  // a byte per row: the largest scale, 255 - the smallest
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 c = st.codes[i][lane];
+        const uint32_t e = (sw[i] >> (8 * t)) & 0xFFu;
+        if ((c.x | c.y | c.z | c.w) & 0x77777777u) {
+          top |= e << (8 * i);
+          low |= (255u - e) << (8 * i);
+        }
+      }
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        top = __vmaxu4(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        low = __vmaxu4(low, __shfl_xor_sync(0xFFFFFFFFu, low, d));
+      }
+      bool apart = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) apart |= ((top >> (8 * i)) & 0xFFu) + ((low >> (8 * i)) & 0xFFu) > 255u + 23u;
+      if (__any_sync(0xFFFFFFFFu, apart)) return step_f16_apart<MT, SCALED>(acc, st, x, undo);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = max(int((top >> (8 * i)) & 0xFFu), 1);
+        f[i][0] = f[i][1] = f16_pow2(int((sw[i] >> (8 * t)) & 0xFFu) - r);
+        ref[i] = __uint_as_float(uint32_t(r) << 23);
+      }
+    }
+  }
+  float part[MT][2][4];
+  const uint4 cw[4] = {st.codes[0][lane], st.codes[1][lane], st.codes[2][lane], st.codes[3][lane]};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t a[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = q == 0 ? cw[i].x : q == 1 ? cw[i].y : q == 2 ? cw[i].z : cw[i].w;
+      widen(w, a[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[i][j] = mul_f16x2(a[i][j], f[i][q >> 1]);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const uint4 b = *reinterpret_cast<const uint4*>(x[m] + q * 64);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (q == 0)
+          mma_f16_first(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
+        else
+          mma_f16(part[m][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
+        mma_f16(part[m][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    float2 out = make_float2(1.f, 1.f);
+    if (SCALED) out = *reinterpret_cast<const float2*>(undo + m * 8);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float v = part[m][h][c], o = c & 1 ? out.y : out.x;
+        float& to = acc[m].v[h][c];
+        if (VIEW == kE8M0x32)
+          to = fmaf(SCALED ? v * o : v, ref[2 * h + (c >> 1)], to);
+        else
+          to = SCALED ? fmaf(v, o, to) : to + v;
+      }
+  }
 }
 
 // One step with bf16 operands: the widened codes' 2^-126 is taken out by the scale's factor
