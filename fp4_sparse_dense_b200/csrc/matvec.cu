@@ -304,25 +304,22 @@ __device__ __forceinline__ void step_f16(Acc (&acc)[MT], const Stage& st, const 
   }
 }
 
-// One step with bf16 operands: the widened codes' 2^-126 is taken out by the scale's factor
-// (E4M3: sf * 2^118, finite up to 448; E8M0: 2^(126 + b - b_max)), the rest with the sum.
-// The codes go in step_f16's order, so that both kinds of operands give the same bits.
+// One step with bf16 operands: the widened codes' 2^-126 is taken out by the scale's factor (E4M3:
+// sf * 2^118, finite up to 448; the rest with the sum) or, for E8M0, before the scale itself is
+// multiplied in: bf16 has float32's exponents, so the operand is the weight as it is, however far
+// apart the scales are. The codes go in step_f16's order, so that both kinds of operands give the
+// same bits where step_f16 takes a step in one pass.
 template <int MT, int VIEW>
 __device__ __forceinline__ void step_bf16(Acc (&acc)[MT], const Stage& st, const uint8_t* const (&x)[MT]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint4 sv = st.scales[VIEW == kE4M3x16 ? t >> 1 : 0][g];
   const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
   uint32_t f[4][2];
-  float ref[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (VIEW == kE8M0x32) {
-      const int b0 = sw[i] & 0xFFu, b1 = (sw[i] >> 8) & 0xFFu, b2 = (sw[i] >> 16) & 0xFFu,
-                b3 = sw[i] >> 24;
-      const int top = max(max(max(b0, b1), max(b2, b3)), 1);
-      f[i][0] = f[i][1] =
-          uint32_t(max(int((sw[i] >> (8 * t)) & 0xFFu) - top + 253, 0)) * 0x00800080u;
-      ref[i] = __uint_as_float(uint32_t(top) << 23);
+      const uint32_t e = (sw[i] >> (8 * t)) & 0xFFu;
+      f[i][0] = f[i][1] = e ? e * 0x00800080u : 0x00400040u;  // 2^(e - 127)
     } else {
 #pragma unroll
       for (int j = 0; j < (VIEW == kE4M3x16 ? 2 : 1); ++j) {
@@ -332,7 +329,6 @@ __device__ __forceinline__ void step_bf16(Acc (&acc)[MT], const Stage& st, const
         asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(f[i][j]) : "f"(v));
       }
       if (VIEW != kE4M3x16) f[i][1] = f[i][0];
-      ref[i] = 256.f;
     }
   }
   float part[MT][2][4];
@@ -346,7 +342,10 @@ __device__ __forceinline__ void step_bf16(Acc (&acc)[MT], const Stage& st, const
       uint32_t h[4];
       widen_bf16(reinterpret_cast<const uint32_t*>(&st.codes[i][lane])[q], h);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = mul_bf16x2(h[j], q < 2 ? f[i][0] : f[i][1]);
+      for (int j = 0; j < 4; ++j) {
+        if (VIEW == kE8M0x32) h[j] = mul_bf16x2(h[j], 0x7E807E80u);  // 2^126
+        h[j] = mul_bf16x2(h[j], q < 2 ? f[i][0] : f[i][1]);
+      }
       a[i][0] = __byte_perm(h[0], h[1], 0x5410);
       a[i][1] = __byte_perm(h[2], h[3], 0x5410);
       a[i][2] = __byte_perm(h[0], h[1], 0x7632);
@@ -368,7 +367,8 @@ __device__ __forceinline__ void step_bf16(Acc (&acc)[MT], const Stage& st, const
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        acc[m].v[h][c] = fmaf(part[m][h][c], ref[2 * h + (c >> 1)], acc[m].v[h][c]);
+        acc[m].v[h][c] = VIEW == kE8M0x32 ? acc[m].v[h][c] + part[m][h][c]
+                                          : fmaf(part[m][h][c], 256.f, acc[m].v[h][c]);
 }
 
 // A lane's sums of a whole unit -> Y, at the lane's first output and row.

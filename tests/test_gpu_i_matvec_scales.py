@@ -122,3 +122,25 @@ def test_scales_apart(M, apart, dtype):
     v64 = v.double().cpu().numpy()
     for r in range(M):
         check(y[r:r + 1], v64[r:r + 1], w64, "f32")
+
+
+@pytest.mark.parametrize("M", [2, 8, 13, 20])
+def test_scales_apart_beside_a_wide_row(M):
+    """Rows that see only blocks of scale 2^-107 beside others of 2^53, in a call with a row whose
+    activations do not fit f16."""
+    import fp4_sparse_dense_b200 as sq
+    import torch
+    rng = np.random.default_rng(M)
+    K, N = 512, 128
+    raw = np.full((N, K // 32), 180, np.uint8)
+    raw[:, 1::4] = 20
+    w, w64 = with_scales(rng, raw)
+    x = torch.from_numpy(rng.standard_normal((M, K))).to(torch.bfloat16)
+    small = torch.from_numpy(np.arange(K) // 32 % 4 == 1)
+    x[1:, ~small] = 0
+    x[0] = 0
+    x[0, 40], x[0, 5] = 1e30, 1e-8
+    x64 = x.double().numpy()
+    y = sq.matvec(x.cuda(), w, out_dtype=torch.float32)
+    for r in range(M):
+        check(y[r:r + 1], x64[r:r + 1], w64, "f32")
