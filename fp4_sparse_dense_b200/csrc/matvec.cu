@@ -44,9 +44,10 @@
 //   of zeros (their scale byte is 0) do not count. A wider spread takes a pass per block of 32 K.
 // - fp16 activations enter as they are. bf16 ones are scaled by a power of two per (row,
 //   step) so that the largest one's exponent is 15; exact for 32 binades, and the scale is
-//   taken out with the step's sum. Where some (row, step) of a CTA has a wider spread, or
-//   infinite or NaN values, the CTA's activations stay bf16 and the codes are widened to bf16
-//   by shifts and masks (about twice the instructions).
+//   taken out with the step's sum. Where some (row, step) of a CTA has a wider spread, infinite
+//   or NaN values or, beside E8M0 scales, a largest value outside 2^-63 ... 2^64, the CTA's
+//   activations stay bf16 and the codes are widened to bf16 by shifts and masks (about twice the
+//   instructions).
 // So every product is exact. The MMA's own additions cut bits below the accumulator's 24, so
 // an accumulator lives for one step (8 MMAs) and joins a float32 sum that rounds to nearest.
 #include <atomic>
@@ -103,9 +104,15 @@ struct Stage {
   uint4 scales[2][8];
 };
 
+// E8M0 scales and largest activations whose product's exponent fits float32: bytes (exponents)
+// of kMiddle ... 254 - kMiddle. Their powers of two multiply to 2^-141 ... 2^111.
+constexpr int kMiddle = 64;
+
 // Eight bf16 activations of a (row, step) whose sixteen lanes call together -> f16, scaled by
 // a power of two; *undo takes it out again. *wide: their spread does not fit (infinite and
-// NaN values never do).
+// NaN values never do). MIDDLE: nor does a largest value outside 2^-63 ... 2^64, so that *undo
+// times a scale of that range (step_f16) is a float32 whatever they are.
+template <bool MIDDLE>
 __device__ __forceinline__ uint4 scale_bf16(uint4 v, float* undo, bool* wide) {
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
   // largest magnitude, and 0xFFFF - (smallest non-zero one - 1), as 16-bit patterns
@@ -122,7 +129,7 @@ __device__ __forceinline__ uint4 scale_bf16(uint4 v, float* undo, bool* wide) {
   // subnormals count as the smallest normal exponent: their bits lie no deeper than its
   const int top = max(int(key & 0xFFFFu) >> 7, 1);
   const int low = max(int(0x10000u - (key >> 16)) >> 7, 1);  // no value but 0: 512
-  *wide = top - low >= 32 || top == 255;
+  *wide = top - low >= 32 || top == 255 || (MIDDLE && low < 512 && uint32_t(top - kMiddle) > 254u - 2 * kMiddle);
   const int shift = min(142 - top, 126);  // the largest exponent to 15
   *undo = pow2_normal(-shift);
   const uint32_t f = uint32_t(shift + 127) * 0x00800080u;
@@ -218,11 +225,12 @@ __device__ __forceinline__ void step_f16(Acc (&acc)[MT], const Stage& st, const 
       f[i + 1][0] = f[i + 1][1] = __byte_perm(two, two, 0x3232);
     }
   } else {
+    constexpr uint32_t kLeast = SCALED ? kMiddle : 1, kMost = 254 - kMiddle;  // of the scale left out
     uint32_t off = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int d = int((sw[i] >> (8 * t)) & 0xFFu) - int(sw[i] & 0xFFu);
-      off |= uint32_t(d + 14) > 27u || ((sw[i] & 0xFFu) - 1u) > 189u;
+      off |= uint32_t(d + 14) > 27u || (sw[i] & 0xFFu) - kLeast > kMost - kLeast;
     }
     if (__all_sync(0xFFFFFFFFu, off == 0)) {
 #pragma unroll
@@ -251,11 +259,15 @@ __device__ __forceinline__ void step_f16(Acc (&acc)[MT], const Stage& st, const 
       }
       bool apart = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) apart |= ((top >> (8 * i)) & 0xFFu) + ((low >> (8 * i)) & 0xFFu) > 255u + 23u;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t most = (top >> (8 * i)) & 0xFFu;
+        apart |= most + ((low >> (8 * i)) & 0xFFu) > 255u + 23u;
+        apart |= SCALED && ((low >> (8 * i)) & 0xFFu) != 0 && most - kLeast > kMost - kLeast;
+      }
       if (__any_sync(0xFFFFFFFFu, apart)) return step_f16_apart<MT, SCALED>(acc, st, x, undo);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = max(int((top >> (8 * i)) & 0xFFu), 1);
+        const int r = max(int((top >> (8 * i)) & 0xFFu), int(kLeast));  // less: zeros only, or 2^-127
         f[i][0] = f[i][1] = f16_pow2(int((sw[i] >> (8 * t)) & 0xFFu) - r);
         ref[i] = __uint_as_float(uint32_t(r) << 23);
       }
@@ -296,8 +308,9 @@ __device__ __forceinline__ void step_f16(Acc (&acc)[MT], const Stage& st, const 
       for (int c = 0; c < 4; ++c) {
         const float v = part[m][h][c], o = c & 1 ? out.y : out.x;
         float& to = acc[m].v[h][c];
+        // the two powers of two first: the sum times either alone may leave float32
         if (VIEW == kE8M0x32)
-          to = fmaf(SCALED ? v * o : v, ref[2 * h + (c >> 1)], to);
+          to = fmaf(v, SCALED ? o * ref[2 * h + (c >> 1)] : ref[2 * h + (c >> 1)], to);
         else
           to = SCALED ? fmaf(v, o, to) : to + v;
       }
@@ -585,7 +598,7 @@ stream_kernel(const MatvecParams p) {
         if (convert) {
           float undo;
           bool wide;
-          v[b] = scale_bf16(v[b], &undo, &wide);
+          v[b] = scale_bf16<VIEW == kE8M0x32>(v[b], &undo, &wide);
           if (c == 0 && at[b] >= 0) {
             s_undo[ss * R + rr] = undo;
             any_wide |= wide;

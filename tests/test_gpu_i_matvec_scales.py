@@ -144,3 +144,20 @@ def test_scales_apart_beside_a_wide_row(M):
     y = sq.matvec(x.cuda(), w, out_dtype=torch.float32)
     for r in range(M):
         check(y[r:r + 1], x64[r:r + 1], w64, "f32")
+
+
+@pytest.mark.parametrize("x_size,w_size", [(1e37, 0.02), (1e36, 1e-15), (1e-37, 1e20), (1e-30, 1e25), (1e30, 1e-30),
+                                           (1e-38, 1e38), (1e3, 1e-38)])
+@pytest.mark.parametrize("M", [1, 8, 12, 20])
+def test_large_and_small_magnitudes(M, x_size, w_size):
+    """bf16 activations and MXFP4 weights anywhere in their range: what a float32 product holds,
+    the call holds."""
+    import fp4_sparse_dense_b200 as sq
+    import torch
+    rng = np.random.default_rng(M)
+    K, N = 512, 128
+    w, w64 = quantised((rng.standard_normal((K, N)) * w_size).clip(-3e38, 3e38).astype(np.float32))
+    x = torch.from_numpy(rng.standard_normal((M, K)) * x_size).to(torch.bfloat16)
+    x64 = x.double().numpy()
+    assert np.abs(x64 @ w64.T).max() < 2.0 ** 127 and np.abs(x64 @ w64.T).min() > 2.0 ** -126
+    check(sq.matvec(x.cuda(), w, out_dtype=torch.float32), x64, w64, "f32")
