@@ -491,9 +491,13 @@ sharq_status check_tokens(const sharq_tokens* t) {
   return SHARQ_OK;
 }
 
-// One [.][H] matrix of the row moves.
+// One [.][H] matrix of the row moves. Their kernels' column index goes up to a stride (8192 at
+// most) beyond the row's end and has to stay a 32-bit number.
+constexpr int32_t kMaxRow = INT32_MAX - 65535;
+
 sharq_status check_rows(const void* m, size_t ld, int32_t H, sharq_dtype dtype) {
   if (!m || H < 1 || ld < size_t(H) || !is_dtype(dtype)) return SHARQ_ERR_INVALID_ARG;
+  if (H > kMaxRow) return SHARQ_ERR_UNSUPPORTED;
   return aligned_to(m, element_bytes(dtype)) ? SHARQ_OK : SHARQ_ERR_MISALIGNED;
 }
 

@@ -312,8 +312,9 @@ typedef struct {
 /* Sorts the assignments by expert (stable: equal experts keep the order of a) and, where X is
  * not null, gathers rows[p] = X[order[p] / k] for p < offsets[E]; rows behind that are left
  * as they were. experts: device [T][k] int32 (id_bits 32) or int64 (64); an id outside
- * [0, E) is dropped. X: device [T][H], rows: device [T * k][H], any H >= 1, dtype F16, BF16
- * or F32, aligned to their elements (16-byte rows are fastest). */
+ * [0, E) is dropped. X: device [T][H], rows: device [T * k][H], 1 <= H <= 2^31 - 65536 (here and
+ * below; longer: SHARQ_ERR_UNSUPPORTED), dtype F16, BF16 or F32, aligned to their elements
+ * (16-byte rows are fastest). */
 SHARQ_API sharq_status sharq_sort_tokens(const void* experts, int32_t id_bits,
                                          const sharq_tokens* tokens, const void* X, size_t ldx,
                                          int32_t H, sharq_dtype dtype, void* rows,
