@@ -18,9 +18,7 @@ from __future__ import annotations
 from ctypes import byref
 from dataclasses import dataclass
 
-import torch
-
-from . import (BF16, Config, F16, F32, QuantWeight, _CStructCache, _ptr, check,
+from . import (BF16, Config, F16, F32, QuantWeight, _CStructCache, _ptr, _torch, check,
                quantize_weight)
 from ._abi import (
     sharq_combine_tokens as _combine_tokens, sharq_combine_tokens_backward as _combine_tokens_backward,
@@ -28,11 +26,20 @@ from ._abi import (
     sharq_sort_tokens as _sort_tokens, sharq_tokens, sharq_weight_bytes, sharq_weight_sizes,
 )
 
-_DTYPE = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+# bound by _load: importing the package takes neither torch nor a CUDA build of it
+torch = _current_device = _current_stream = None
+_DTYPE = {}
 
 
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+def _load():
+    """Binds torch and its two cheapest queries on first use (a CPU build has no queries, and no
+    CUDA tensors to ask about)."""
+    global torch, _current_device, _current_stream
+    t = _torch()
+    _DTYPE.update({t.bfloat16: BF16, t.float16: F16, t.float32: F32})
+    _current_device = getattr(t._C, "_cuda_getDevice", None)
+    _current_stream = getattr(t._C, "_cuda_getCurrentRawStream", None)
+    torch = t
 
 
 def _elsewhere(device, stream) -> bool:
@@ -51,6 +58,8 @@ def _on(device, stream):
 
 
 def _cuda(name, x, device=None):
+    if torch is None:
+        _load()
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if device is not None and x.device != device:
@@ -167,6 +176,7 @@ class ExpertWeights(_CStructCache):
     cfg: Config
 
     def _make_c(self) -> sharq_expert_weights:
+        torch = _torch()
         sz = self._bytes()
         for name in ("codes", "scales_dense", "scales_sparse"):
             t, n = getattr(self, name), getattr(sz, name)
@@ -234,6 +244,7 @@ class SortedTokens(_CStructCache):
     E: int
 
     def _make_c(self) -> sharq_tokens:
+        torch = _torch()
         n = self.T * self.k
         for name, want in (("offsets", self.E + 1), ("order", n), ("place", n)):
             t = getattr(self, name)

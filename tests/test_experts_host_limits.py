@@ -1,6 +1,9 @@
 """Refusals at the limits of the experts' operators, and what importing the package takes (no GPU
 is touched)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -21,3 +24,70 @@ def test_rows_beyond_a_32_bit_column_are_refused(sq, H, dtype):  # noqa: F811
     # the longest row passes these checks: the next one, alignment, answers
     n = 2 ** 31 - 65536
     assert sq.sharq_combine_tokens(P + 1, n, n, dtype, b, P, P, n, None) == 3
+
+
+def run_python(code):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    return r.stdout
+
+
+NO_TORCH = """
+import sys
+class NoTorch:
+    def find_spec(self, name, path=None, target=None):
+        if name.split(".")[0] == "torch":
+            raise ModuleNotFoundError(name)
+sys.meta_path.insert(0, NoTorch())
+"""
+
+SIZES = """
+import ctypes
+import fp4_sparse_dense_b200 as sq
+sz = sq.sharq_weight_bytes()
+assert sq.sharq_weight_sizes(256, 128, sq.Config().c(), ctypes.byref(sz)) == 0 and sz.codes == 16384
+t = sq.sharq_tokens(None, None, None, 0, 1, 1)
+assert sq.sharq_sort_tokens(None, 64, ctypes.byref(t), None, 0, 0, 1, None, 0, None) == 1
+"""
+
+
+def test_the_package_imports_without_torch(sq):  # noqa: F811
+    """The C names and the size queries need no torch; the tensor helpers are named all the same."""
+    run_python(NO_TORCH + SIZES + "from fp4_sparse_dense_b200 import *\nassert matvec and SortedTokens")
+
+
+def test_importing_the_package_does_not_import_torch(sq):  # noqa: F811
+    run_python("import sys\n" + SIZES + "assert 'torch' not in sys.modules")
+
+
+def test_helpers_refuse_cpu_tensors_on_a_cpu_build_of_torch(sq):  # noqa: F811
+    """A build without CUDA has neither of the queries that the helpers use."""
+    run_python("""
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import fp4_sparse_dense_b200 as sq
+try:
+    sq.matvec(torch.zeros(1, 256, dtype=torch.bfloat16), None)
+except ValueError as e:
+    assert "CUDA" in str(e)
+else:
+    raise AssertionError
+""")
+
+
+@pytest.mark.parametrize("first", ["sq.SortedTokens(i(5), i(4), i(2, 2), 2, 2, 4).c",
+                                   "sq.ExpertWeights(None, None, None, torch.zeros(4), 256, 128, 1, sq.Config()).c"])
+def test_structs_check_their_buffers_before_any_call(sq, first):  # noqa: F811
+    """The checks work whatever is called first: these refuse CPU tensors and missing buffers."""
+    run_python("""
+import torch
+import fp4_sparse_dense_b200 as sq
+i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+try:
+    %s()
+except ValueError:
+    pass
+""" % first)
