@@ -79,11 +79,12 @@ struct StreamKeyHash {
     return size_t(k.ctx * 0x9E3779B97F4A7C15ull) ^ reinterpret_cast<size_t>(k.stream);
   }
 };
-// Per stream: its status slot, and whether the GEMM may load its weight before waiting for
+// Per stream: its status slot, and whether a product may load its weight before waiting for
 // the kernel launched just before it. That holds when the last launch of this library on the
-// stream was a preparation or a linear call: each of their kernels waits for its own
-// predecessor before it lets a dependent start, and none of them writes a weight. It does not
-// hold on a stream not seen before, nor after sharq_quantize_weight.
+// stream was any but sharq_quantize_weight (a preparation, a linear call, a few-row product, a
+// sort, a combination): each of their kernels waits for its own predecessor before it lets a
+// dependent start, and none of them writes a weight. It does not hold on a stream not seen
+// before, nor after a launch that failed.
 struct StreamState {
   int slot = 0;
   bool weight_early = false;
@@ -159,6 +160,13 @@ bool note_launch(const DeviceInfo& d, cudaStream_t stream, bool weight_early_aft
   const bool before = st.weight_early;
   st.weight_early = weight_early_after;
   return before;
+}
+
+// The status of a launch that note_launch has allowed early loads after. A launch that failed
+// allows none: the kernel before it may have written a weight.
+sharq_status noted(const DeviceInfo& d, cudaStream_t stream, sharq_status launch) {
+  if (launch != SHARQ_OK) note_launch(d, stream, false);
+  return launch;
 }
 
 unsigned int* status_word(const DeviceInfo& d, cudaStream_t stream) {
@@ -478,8 +486,8 @@ sharq_status run_matvec(MatvecParams* p, bool bf16, ScaleView view, const Device
     p->timeout_ns = kWaitLimitNs;
   }
   p->early = note_launch(d, st, true) ? 1 : 0;
-  return from_cuda(tiles ? launch_matvec_tiles(map, *p, bf16, view, d.num_sms, d.ctx_id, st)
-                         : launch_matvec(*p, bf16, view, d.num_sms, d.ctx_id, st));
+  return noted(d, st, from_cuda(tiles ? launch_matvec_tiles(map, *p, bf16, view, d.num_sms, d.ctx_id, st)
+                                      : launch_matvec(*p, bf16, view, d.num_sms, d.ctx_id, st)));
 }
 
 sharq_status check_tokens(const sharq_tokens* t) {
@@ -779,9 +787,9 @@ sharq_status sharq_linear(const sharq_act* a, const sharq_weight* w, void* Y, sh
   // is one of this library's that writes no weight (see StreamState)
   const bool weight_early = note_launch(d, st, true);
   p.prefetch_w = (M < 256 && weight_early) ? 1 : 0;
-  if (own) return from_cuda(launch_gemm_two(maps, p, y_dtype == SHARQ_F32, d.num_sms, st));
-  return from_cuda(launch_gemm(maps, p, a->cfg.fmt, a->cfg.mask, res, y_dtype == SHARQ_F32,
-                               d.num_sms, st));
+  if (own) return noted(d, st, from_cuda(launch_gemm_two(maps, p, y_dtype == SHARQ_F32, d.num_sms, st)));
+  return noted(d, st, from_cuda(launch_gemm(maps, p, a->cfg.fmt, a->cfg.mask, res, y_dtype == SHARQ_F32,
+                                            d.num_sms, st)));
 }
 
 sharq_status sharq_matvec(const void* X, size_t ldx, int32_t M, sharq_dtype dtype,
