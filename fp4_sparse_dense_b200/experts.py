@@ -134,6 +134,10 @@ def matvec(X, w: QuantWeight, out=None, out_dtype=None, stream=None):
     `out_dtype` (default: X's; also float32). For the few rows of a decode step, where the
     weight's bytes set the time; the activations are not quantised. For many rows ``prepare``
     + ``linear`` is faster.
+
+    The weight may be loaded before the kernel launched just before has completed, unless that
+    was ``quantize_weight``. A kernel of one's own that writes w's buffers in place must not come
+    directly before this call; copies, or a write ordered through an event, are fine.
     """
     _cuda("X", X)
     device = X.device

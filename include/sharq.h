@@ -224,11 +224,14 @@ SHARQ_API sharq_status sharq_prepare_rmsnorm(const void* X, const void* gamma, f
  * Ordering: the GEMM is launched as a programmatic dependent of the kernel launched just
  * before it on `stream`. It reads nothing of *act before that kernel has completed. For
  * M < 256 it may start loading w's codes and scales while that kernel still runs, when
- * this library's previous launch on `stream` was a preparation or a linear call. It does
- * not do this on a stream it has not seen before, nor after sharq_quantize_weight. So w
- * must be complete before the kernel launched just before this call starts. A caller's
- * own kernel that writes w must not come between a preparation and this call on `stream`.
- * A copy (cudaMemcpyAsync) or a write ordered through an event is fine. */
+ * this library's previous launch on `stream` was a preparation, a linear call, or any of
+ * sharq_matvec, sharq_expert_matvec, sharq_sort_tokens, sharq_combine_tokens and their
+ * gradients. It does not do this on a stream it has not seen before, nor after
+ * sharq_quantize_weight or a launch that failed. So w must be complete before the kernel
+ * launched just before this call starts. A caller's own kernel that writes w must not come
+ * between one of those calls and this one on `stream`. A copy (cudaMemcpyAsync) or a write
+ * ordered through an event is fine. A call that is captured counts as a launch on its stream:
+ * synchronise a stream on which sharq_quantize_weight still runs before capturing on it. */
 SHARQ_API sharq_status sharq_linear(const sharq_act* act, const sharq_weight* w, void* Y,
                                     sharq_dtype y_dtype, void* workspace, size_t workspace_bytes,
                                     void* stream);
@@ -277,9 +280,10 @@ SHARQ_API sharq_status sharq_linear_noalloc(const sharq_act* act, const sharq_we
  * their own row as in a float32 product. The weight is read once per 32 rows: for many rows
  * sharq_prepare + sharq_linear is the faster path. Y overlaps neither X nor w.
  * M <= 2^21 (else SHARQ_ERR_UNSUPPORTED).
- * Ordering: as sharq_linear's; here the weight may be loaded early at every M. Calls with more
- * than 16 rows (or too long a K for fewer) use tensor memory and bounded waits; a wait that runs
- * out is reported by sharq_read_device_status, and Y is then incomplete. */
+ * Ordering: as sharq_linear's, and here the weight may be loaded early at every M: a caller's own
+ * kernel that writes w must not come between this library's previous launch on `stream` and this
+ * call. Calls with more than 16 rows (or too long a K for fewer) use tensor memory and bounded
+ * waits; a wait that runs out is reported by sharq_read_device_status, and Y is then incomplete. */
 SHARQ_API sharq_status sharq_matvec(const void* X, size_t ldx, int32_t M, sharq_dtype dtype,
                                     const sharq_weight* w, void* Y, size_t ldy,
                                     sharq_dtype y_dtype, void* stream);
