@@ -30,6 +30,9 @@ from ._abi import (
 torch = _current_device = _current_stream = None
 _DTYPE = {}
 
+_INVALID_ARG, _UNSUPPORTED = 1, 2  # sharq_status
+_INT32_MAX = 2 ** 31 - 1
+
 
 def _load():
     """Binds torch and its two cheapest queries on first use (a CPU build has no queries, and no
@@ -103,6 +106,8 @@ def _readable(name, x, align16=False):
     if x.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got {list(x.shape)}")
     rows, cols = x.shape
+    if rows > _INT32_MAX or cols > _INT32_MAX:  # ctypes would cut them to 32 bits
+        raise ValueError(f"{name} must be smaller than 2^31 rows and columns, got {list(x.shape)}")
     if x.is_contiguous():
         ld, ok = cols, True
     else:
@@ -249,6 +254,7 @@ class SortedTokens(_CStructCache):
 
     def _make_c(self) -> sharq_tokens:
         torch = _torch()
+        _assignments(self.T, self.k, self.E)
         n = self.T * self.k
         for name, want in (("offsets", self.E + 1), ("order", n), ("place", n)):
             t = getattr(self, name)
@@ -257,6 +263,15 @@ class SortedTokens(_CStructCache):
             _cuda(name, t, self.offsets.device)
         return sharq_tokens(_ptr(self.offsets), _ptr(self.order), _ptr(self.place),
                             self.T, self.k, self.E)
+
+
+def _assignments(T, k, E):
+    """Raises what the C call answers to these sizes: before anything of them is allocated, and
+    before ctypes cuts them to 32 bits."""
+    if T < 0 or k < 1 or E < 1:
+        check(_INVALID_ARG)
+    if E > 1024 or T * k >= 1 << 30:
+        check(_UNSUPPORTED)
 
 
 def _empty_tokens(T, k, E, like) -> SortedTokens:
@@ -292,6 +307,7 @@ def sort_tokens(experts, num_experts: int, X=None, rows=None, out: SortedTokens 
     else:
         raise TypeError(f"unsupported dtype {experts.dtype} of experts (need int32 or int64)")
     T, k = experts.shape
+    _assignments(T, k, num_experts)
     if not experts.is_contiguous():
         experts = experts.contiguous()
     if out is None:
