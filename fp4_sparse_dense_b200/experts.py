@@ -11,7 +11,10 @@ layer of experts as
 
 Every call runs on the device of its tensors and on ``stream`` (default: that device's
 current stream); outputs it allocates belong to that stream. Bad arguments raise ValueError
-or TypeError here, or SharqError with the C status.
+or TypeError here, or SharqError with the C status. What a call writes (``out``, ``rows``,
+``d_rows``, ``d_weights``) overlaps nothing that it reads, except that ``d_rows`` may be
+``rows``. No call records an autograd graph: its outputs do not require gradients, and the
+gradients are calls of their own.
 """
 from __future__ import annotations
 
@@ -135,8 +138,8 @@ def _new(like, rows, cols, dtype=None):
 def matvec(X, w: QuantWeight, out=None, out_dtype=None, stream=None):
     """Y[M x N] = X[M x K] deq(w) with the activations left in 16 bits (``sharq_matvec``).
 
-    X: CUDA tensor [M x K], bf16 or fp16 (rows may be strided). Y is `out`, or a new tensor of
-    `out_dtype` (default: X's; also float32). For the few rows of a decode step, where the
+    X: CUDA tensor [M x K], bf16 or fp16 (rows may be strided). Y is `out` (its first element
+    16-byte aligned), or a new tensor of `out_dtype` (default: X's; also float32). For the few rows of a decode step, where the
     weight's bytes set the time; the activations are not quantised. For many rows ``prepare``
     + ``linear`` is faster.
 
@@ -348,8 +351,8 @@ def expert_matvec(X, w: ExpertWeights, tokens: SortedTokens, gather: bool = Fals
                   out_dtype=None, stream=None):
     """Y[p] = X row of sorted row p times its expert's weight (``sharq_expert_matvec``), the
     activations left in 16 bits. X: the sorted rows [T * k, K], or with gather=True the tokens
-    [T, K]. Returns Y [T * k, N] (`out`, or a new tensor of `out_dtype`, default X's); rows
-    behind the last kept assignment are left as they were (undefined in a new tensor)."""
+    [T, K]. Returns Y [T * k, N] (`out`, its first element 16-byte aligned, or a new tensor of
+    `out_dtype`, default X's); rows behind the last kept assignment are left as they were (undefined in a new tensor)."""
     _cuda("X", X)
     device = X.device
     if _elsewhere(device, stream):

@@ -270,16 +270,21 @@ SHARQ_API sharq_status sharq_linear_noalloc(const sharq_act* act, const sharq_we
  * These calls (no counterpart in the SharQ page) use the weight payload above without
  * preparing the activations: a decoded token's row goes into the product as it is. Their
  * matrices have a row pitch in elements (ld >= the row's length), so a view of a larger
- * matrix can be passed. T = 0 or no rows at all is allowed and writes nothing but offsets. */
+ * matrix can be passed. T = 0 or no rows at all is allowed and writes nothing but offsets.
+ * What a call writes overlaps nothing that it reads, except where the call says so. */
 
 /* Y[M x N] = s_gw * X[M x K] * deq(W): the activations stay in 16 bits. Products are exact
  * (E2M1 * scale has at most 6 significant bits), sums are float32 in a fixed order, and Y is
- * rounded once. X: device [M][K], `dtype` F16 or BF16, 16-byte aligned, ldx % 8 == 0. w: any
- * configuration; pair masks are read through scales_sparse, the others through scales_dense.
- * Y: device [M][N], F16, BF16 or F32. Infinite and NaN activations reach the outputs of
- * their own row as in a float32 product. The weight is read once per 32 rows: for many rows
- * sharq_prepare + sharq_linear is the faster path. Y overlaps neither X nor w.
- * M <= 2^21 (else SHARQ_ERR_UNSUPPORTED).
+ * rounded once. The sums are taken before s_gw is multiplied in (up to 2688 / amax|W| times Y for
+ * NVFP4) and have to fit float32 there. X: device [M][K], `dtype` F16 or BF16, 16-byte aligned,
+ * ldx % 8 == 0. w: any configuration; pair masks are read through scales_sparse, the others
+ * through scales_dense. Y: device [M][N], F16, BF16 or F32, 16-byte aligned with any ldy >= N
+ * (else SHARQ_ERR_MISALIGNED). Infinite and NaN activations reach the outputs of their own row as
+ * in a float32 product. The weight is read once per 32 rows at most: for many rows
+ * sharq_prepare + sharq_linear is the faster path. M <= 2^21 (else SHARQ_ERR_UNSUPPORTED).
+ * The same call gives the same bits every time. The split of K, and with it the order of a row's
+ * sum, goes by M and K, and activations of one row that do not fit f16 send those beside them
+ * through bf16 operands, so a row's last bits may depend on the rows that it comes with.
  * Ordering: as sharq_linear's, and here the weight may be loaded early at every M: a caller's own
  * kernel that writes w must not come between this library's previous launch on `stream` and this
  * call. Calls with more than 16 rows (or too long a K for fewer) use tensor memory and bounded
@@ -333,7 +338,7 @@ SHARQ_API sharq_status sharq_sort_tokens_backward(const void* d_rows, size_t ld_
 /* Y[p] = X row of sorted row p * deq(W of its expert), as sharq_matvec, for p < offsets[E];
  * rows behind that are left as they were. gather == 0: X holds the sorted rows [T * k][K];
  * gather == 1: X holds the tokens [T][K] and row p reads token order[p] / k. tokens->E must
- * equal w->E. The number of rows is known on the device only, so nothing of the weight is loaded
+ * equal w->E; Y is 16-byte aligned. The number of rows is known on the device only, so nothing of the weight is loaded
  * before the kernel launched just before this call has completed. T * k <= 2^19 and E * N < 2^31
  * (else SHARQ_ERR_UNSUPPORTED). */
 SHARQ_API sharq_status sharq_expert_matvec(const void* X, size_t ldx, int32_t gather,
