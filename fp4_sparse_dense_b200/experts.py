@@ -139,9 +139,9 @@ def matvec(X, w: QuantWeight, out=None, out_dtype=None, stream=None):
     """Y[M x N] = X[M x K] deq(w) with the activations left in 16 bits (``sharq_matvec``).
 
     X: CUDA tensor [M x K], bf16 or fp16 (rows may be strided). Y is `out` (its first element
-    16-byte aligned), or a new tensor of `out_dtype` (default: X's; also float32). For the few rows of a decode step, where the
-    weight's bytes set the time; the activations are not quantised. For many rows ``prepare``
-    + ``linear`` is faster.
+    16-byte aligned), or a new tensor of `out_dtype` (default: X's; also float32). For the few
+    rows of a decode step, where the weight's bytes set the time; the activations are not
+    quantised. For many rows ``prepare`` + ``linear`` is faster.
 
     The weight may be loaded before the kernel launched just before has completed, unless that
     was ``quantize_weight``. A kernel of one's own that writes w's buffers in place must not come
@@ -352,7 +352,8 @@ def expert_matvec(X, w: ExpertWeights, tokens: SortedTokens, gather: bool = Fals
     """Y[p] = X row of sorted row p times its expert's weight (``sharq_expert_matvec``), the
     activations left in 16 bits. X: the sorted rows [T * k, K], or with gather=True the tokens
     [T, K]. Returns Y [T * k, N] (`out`, its first element 16-byte aligned, or a new tensor of
-    `out_dtype`, default X's); rows behind the last kept assignment are left as they were (undefined in a new tensor)."""
+    `out_dtype`, default X's); rows behind the last kept assignment are left as they were
+    (undefined in a new tensor)."""
     _cuda("X", X)
     device = X.device
     if _elsewhere(device, stream):

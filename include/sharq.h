@@ -280,7 +280,7 @@ SHARQ_API sharq_status sharq_linear_noalloc(const sharq_act* act, const sharq_we
  * ldx % 8 == 0. w: any configuration; pair masks are read through scales_sparse, the others
  * through scales_dense. Y: device [M][N], F16, BF16 or F32, 16-byte aligned with any ldy >= N
  * (else SHARQ_ERR_MISALIGNED). Infinite and NaN activations reach the outputs of their own row as
- * in a float32 product. The weight is read once per 32 rows at most: for many rows
+ * in a float32 product. The weight is read once for up to 32 rows: for many rows
  * sharq_prepare + sharq_linear is the faster path. M <= 2^21 (else SHARQ_ERR_UNSUPPORTED).
  * The same call gives the same bits every time. The split of K, and with it the order of a row's
  * sum, goes by M and K, and activations of one row that do not fit f16 send those beside them
@@ -338,8 +338,9 @@ SHARQ_API sharq_status sharq_sort_tokens_backward(const void* d_rows, size_t ld_
 /* Y[p] = X row of sorted row p * deq(W of its expert), as sharq_matvec, for p < offsets[E];
  * rows behind that are left as they were. gather == 0: X holds the sorted rows [T * k][K];
  * gather == 1: X holds the tokens [T][K] and row p reads token order[p] / k. tokens->E must
- * equal w->E; Y is 16-byte aligned. The number of rows is known on the device only, so nothing of the weight is loaded
- * before the kernel launched just before this call has completed. T * k <= 2^19 and E * N < 2^31
+ * equal w->E; Y is 16-byte aligned. A weight is read once for up to 8 of its rows (32 where there
+ * are more than 8 per expert on average). The number of rows is known on the device only, so
+ * nothing of the weight is loaded before the kernel launched just before this call has completed. T * k <= 2^19 and E * N < 2^31
  * (else SHARQ_ERR_UNSUPPORTED). */
 SHARQ_API sharq_status sharq_expert_matvec(const void* X, size_t ldx, int32_t gather,
                                            sharq_dtype dtype, const sharq_tokens* tokens,
