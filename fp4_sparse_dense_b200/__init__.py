@@ -26,7 +26,7 @@ from ._abi import (  # noqa: F401
     sharq_read_device_status,
     sharq_prepare, sharq_quantize_weight, sharq_linear, sharq_linear_workspace_size,
     sharq_linear_noalloc, sharq_prepare_rmsnorm, sharq_wait_probe, sharq_prepare_alongside,
-    sharq_prepare_given_amax, sharq_matvec, sharq_sort_tokens, sharq_sort_tokens_backward,
+    sharq_prepare_given_amax, sharq_matvec, sharq_matvec_plan, sharq_sort_tokens, sharq_sort_tokens_backward,
     sharq_expert_matvec, sharq_combine_tokens, sharq_combine_tokens_backward, sharq_tokens,
     sharq_expert_weights,
 )
@@ -41,7 +41,7 @@ __all__ = [
     "NVFP4", "MXFP4", "PAIR_4_8", "ELEM_2_4", "F16", "BF16", "F32",
     "matvec", "ExpertWeights", "quantize_experts", "SortedTokens", "sort_tokens",
     "sort_tokens_backward", "expert_matvec", "combine_tokens", "combine_tokens_backward",
-    "sharq_matvec", "sharq_sort_tokens", "sharq_sort_tokens_backward", "sharq_expert_matvec",
+    "sharq_matvec", "sharq_matvec_plan", "sharq_sort_tokens", "sharq_sort_tokens_backward", "sharq_expert_matvec",
     "sharq_combine_tokens", "sharq_combine_tokens_backward",
 ]
 

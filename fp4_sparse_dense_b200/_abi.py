@@ -87,6 +87,7 @@ def _load():
         "sharq_linear_noalloc": (st, [ctypes.POINTER(sharq_act), ctypes.POINTER(sharq_weight),
                                       vp, ctypes.c_int, vp]),
         "sharq_matvec": (st, [vp, sz, i32, st, ctypes.POINTER(sharq_weight), vp, sz, st, vp]),
+        "sharq_matvec_plan": (st, [i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]),
         "sharq_sort_tokens": (st, [vp, i32, tok, vp, sz, i32, st, vp, sz, vp]),
         "sharq_sort_tokens_backward": (st, [vp, sz, i32, st, tok, vp, sz, vp]),
         "sharq_expert_matvec": (st, [vp, sz, i32, st, tok, ew, vp, sz, st, vp]),
@@ -116,6 +117,7 @@ sharq_linear = lib.sharq_linear
 sharq_linear_workspace_size = lib.sharq_linear_workspace_size
 sharq_linear_noalloc = lib.sharq_linear_noalloc
 sharq_matvec = lib.sharq_matvec
+sharq_matvec_plan = lib.sharq_matvec_plan
 sharq_sort_tokens = lib.sharq_sort_tokens
 sharq_sort_tokens_backward = lib.sharq_sort_tokens_backward
 sharq_expert_matvec = lib.sharq_expert_matvec

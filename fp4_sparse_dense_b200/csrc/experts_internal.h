@@ -45,9 +45,11 @@ cudaError_t launch_matvec(const MatvecParams& p, bool bf16, ScaleView view, int 
 // 64 x 128 with the 64-byte swizzle.
 cudaError_t launch_matvec_tiles(const CUtensorMap& map, MatvecParams p, bool bf16, ScaleView view,
                                 int num_sms, unsigned long long ctx, cudaStream_t st);
-// Whether launch_matvec takes a call: up to 16 rows, or 8 per expert on average, whose activations
-// fit into the shared memory of eight SMs.
-bool matvec_streams(int M, int E, int K);
+// Rows of a slot there.
+int matvec_tile_rows(int M, int E);
+// CTAs over which launch_matvec splits K, 0 where it does not take a call: it takes up to 16 rows, or
+// 8 per expert on average, whose activations fit into the shared memory of eight SMs.
+int matvec_stream_splits(int M, int E, int K);
 
 struct SortParams {
   const void* experts;  // [T * k] int32 or int64

@@ -861,7 +861,10 @@ cudaError_t launch_rows_of(const MatvecParams& p, bool bf16, ScaleView view, int
 
 }  // namespace
 
-bool matvec_streams(int M, int E, int K) { return row_tiles(M, E, K) > 0; }
+int matvec_stream_splits(int M, int E, int K) {
+  const int mt = row_tiles(M, E, K);
+  return mt > 0 ? splits_for(K / kStepK, E > 0 ? kRows : M, E, mt) : 0;
+}
 
 cudaError_t launch_matvec(const MatvecParams& p, bool bf16, ScaleView view, int num_sms,
                           unsigned long long ctx, cudaStream_t st) {

@@ -624,12 +624,16 @@ cudaError_t launch_nc(const CUtensorMap& map, const MatvecParams& p, bool bf16, 
 
 }  // namespace
 
+// 16 or 32 (4096 x 6144, 16 rows: 11.8 us against 12.5; 21 rows: 18.5 against 12.7). An expert's
+// rows are not known here, twice their mean stands for them.
+int matvec_tile_rows(int M, int E) {
+  const int want = E > 0 ? 2 * ((M + E - 1) / E) : M;
+  return want <= 16 ? 16 : 32;
+}
+
 cudaError_t launch_matvec_tiles(const CUtensorMap& map, MatvecParams p, bool bf16, ScaleView view,
                                 int num_sms, unsigned long long ctx, cudaStream_t st) {
-  // Rows per slot: 16 or 32 (4096 x 6144, 16 rows: 11.8 us against 12.5; 21 rows: 18.5 against
-  // 12.7). An expert's rows are not known here, twice their mean stands for them.
-  const int want = p.E > 0 ? 2 * ((p.M + p.E - 1) / p.E) : p.M;
-  const int nc = want <= 16 ? 16 : 32;
+  const int nc = matvec_tile_rows(p.M, p.E);
   unsigned slots = unsigned((p.M + nc - 1) / nc);
   double busy = slots;
   if (p.E > 0) {

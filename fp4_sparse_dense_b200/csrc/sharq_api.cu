@@ -476,7 +476,7 @@ sharq_status matvec_weight(const void* X, size_t ldx, sharq_dtype dtype, void* c
 sharq_status run_matvec(MatvecParams* p, bool bf16, ScaleView view, const DeviceInfo& d,
                         cudaStream_t st) {
   CUtensorMap map;
-  const bool tiles = !matvec_streams(p->M, p->E, p->K);
+  const bool tiles = matvec_stream_splits(p->M, p->E, p->K) == 0;
   if (tiles) {
     const sharq_status s = make_map(&map, p->codes, uint64_t(p->K) / 2,
                                     uint64_t(p->N) * uint64_t(p->E > 0 ? p->E : 1), 64, 128,
@@ -807,6 +807,13 @@ sharq_status sharq_matvec(const void* X, size_t ldx, int32_t M, sharq_dtype dtyp
   if ((s = device_info(&d)) != SHARQ_OK || M == 0) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return run_matvec(&p, dtype == SHARQ_BF16, view, d, st);
+}
+
+sharq_status sharq_matvec_plan(int32_t M, int32_t E, int32_t K, int32_t* tile_rows, int32_t* splits) {
+  if (M < 1 || E < 0 || K < 256 || K % 256 != 0 || !tile_rows || !splits) return SHARQ_ERR_INVALID_ARG;
+  *splits = matvec_stream_splits(M, E, K);
+  *tile_rows = *splits > 0 ? 0 : matvec_tile_rows(M, E);
+  return SHARQ_OK;
 }
 
 sharq_status sharq_expert_matvec(const void* X, size_t ldx, int32_t gather, sharq_dtype dtype,

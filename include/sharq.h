@@ -287,11 +287,19 @@ SHARQ_API sharq_status sharq_linear_noalloc(const sharq_act* act, const sharq_we
  * through bf16 operands, so a row's last bits may depend on the rows that it comes with.
  * Ordering: as sharq_linear's, and here the weight may be loaded early at every M: a caller's own
  * kernel that writes w must not come between this library's previous launch on `stream` and this
- * call. Calls with more than 16 rows (or too long a K for fewer) use tensor memory and bounded
- * waits; a wait that runs out is reported by sharq_read_device_status, and Y is then incomplete. */
+ * call. Calls with more than 16 rows (or too long a K for fewer: sharq_matvec_plan) use tensor
+ * memory and bounded waits; a wait that runs out is reported by sharq_read_device_status, and Y is then incomplete. */
 SHARQ_API sharq_status sharq_matvec(const void* X, size_t ldx, int32_t M, sharq_dtype dtype,
                                     const sharq_weight* w, void* Y, size_t ldy,
                                     sharq_dtype y_dtype, void* stream);
+
+/* Which of two kernels takes a product: E == 0 for sharq_matvec with M rows, else
+ * sharq_expert_matvec with M = T * k over E experts. *tile_rows: 0 where the streaming kernel does,
+ * else the rows (16 or 32) of the tensor-memory kernel's slots. *splits: CTAs that share K in the
+ * streaming kernel (1, 2, 4 or 8), 0 for the other, where that goes by N and the device too. No
+ * GPU needed. INVALID_ARG: M < 1, E < 0, K not a multiple of 256, or an output is NULL. */
+SHARQ_API sharq_status sharq_matvec_plan(int32_t M, int32_t E, int32_t K, int32_t* tile_rows,
+                                         int32_t* splits);
 
 /* The order of T tokens by expert, k assignments each (assignment a = t * k + j). Caller-owned
  * device buffers, filled by sharq_sort_tokens:
@@ -340,8 +348,8 @@ SHARQ_API sharq_status sharq_sort_tokens_backward(const void* d_rows, size_t ld_
  * gather == 1: X holds the tokens [T][K] and row p reads token order[p] / k. tokens->E must
  * equal w->E; Y is 16-byte aligned. A weight is read once for up to 8 of its rows (32 where there
  * are more than 8 per expert on average). The number of rows is known on the device only, so
- * nothing of the weight is loaded before the kernel launched just before this call has completed. T * k <= 2^19 and E * N < 2^31
- * (else SHARQ_ERR_UNSUPPORTED). */
+ * nothing of the weight is loaded before the kernel launched just before this call has completed.
+ * T * k <= 2^19 and E * N < 2^31 (else SHARQ_ERR_UNSUPPORTED). */
 SHARQ_API sharq_status sharq_expert_matvec(const void* X, size_t ldx, int32_t gather,
                                            sharq_dtype dtype, const sharq_tokens* tokens,
                                            const sharq_expert_weights* w, void* Y, size_t ldy,

@@ -91,3 +91,27 @@ try:
 except ValueError:
     pass
 """ % first)
+
+
+def plan(sq, M, E, K):  # noqa: F811
+    tile_rows, splits = ctypes.c_int32(), ctypes.c_int32()
+    assert sq.sharq_matvec_plan(M, E, K, ctypes.byref(tile_rows), ctypes.byref(splits)) == 0
+    return tile_rows.value, splits.value
+
+
+def test_plan_of_the_products(sq):  # noqa: F811
+    """Up to 16 rows (8 per expert on average) stream, over as few CTAs as hold their activations;
+    the rest go to the tiles, in slots of 16 rows where no more are expected."""
+    for M, E, K, want in ((1, 0, 4096, (0, 1)), (8, 0, 4096, (0, 1)), (16, 0, 4096, (0, 2)), (17, 0, 256, (32, 0)), (1 << 21, 0, 256, (32, 0)),
+                          (8, 0, 14336, (0, 4)), (1, 0, 57344, (0, 2)), (16, 0, 19456, (0, 8)), (16, 0, 19712, (16, 0)),
+                          (1, 8, 4096, (0, 1)), (64, 8, 14336, (0, 4)), (65, 8, 4096, (32, 0)), (8, 1, 51200, (16, 0)),
+                          (9, 1, 51200, (32, 0))):
+        assert plan(sq, M, E, K) == want, (M, E, K)
+
+
+def test_plan_refuses(sq):  # noqa: F811
+    a, b = ctypes.c_int32(), ctypes.c_int32()
+    f, r = sq.sharq_matvec_plan, ctypes.byref
+    for M, E, K in ((0, 0, 256), (1, -1, 256), (1, 0, 128), (1, 0, 300), (1, 0, 0)):
+        assert f(M, E, K, r(a), r(b)) == 1
+    assert f(1, 0, 256, None, r(b)) == 1 and f(1, 0, 256, r(a), None) == 1
