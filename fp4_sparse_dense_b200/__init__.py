@@ -118,6 +118,14 @@ class _CStructCache:
         return cs
 
 
+def _one_device(w):
+    """Refuses a weight whose buffers lie on several devices."""
+    for name in ("scales_dense", "scales_sparse", "tensor_scale"):
+        t = getattr(w, name)
+        if t is not None and t.device != w.codes.device:
+            raise ValueError(f"{name} is on {t.device}, codes on {w.codes.device}")
+
+
 @dataclass
 class QuantWeight(_CStructCache):
     codes: object
@@ -129,6 +137,7 @@ class QuantWeight(_CStructCache):
     cfg: Config
 
     def _make_c(self) -> sharq_weight:
+        _one_device(self)
         return sharq_weight(_ptr(self.codes), _ptr(self.scales_dense), _ptr(self.scales_sparse),
                             _ptr(self.tensor_scale), self.K, self.N, self.cfg.c())
 

@@ -21,8 +21,8 @@ from __future__ import annotations
 from ctypes import byref
 from dataclasses import dataclass
 
-from . import (BF16, Config, F16, F32, QuantWeight, _CStructCache, _ptr, _torch, check,
-               quantize_weight)
+from . import (BF16, Config, F16, F32, QuantWeight, _CStructCache, _one_device, _ptr, _torch,
+               check, quantize_weight)
 from ._abi import (
     sharq_combine_tokens as _combine_tokens, sharq_combine_tokens_backward as _combine_tokens_backward,
     sharq_expert_matvec as _expert_matvec, sharq_expert_weights, sharq_matvec as _matvec,
@@ -194,8 +194,10 @@ class ExpertWeights(_CStructCache):
             t, n = getattr(self, name), getattr(sz, name)
             if n and (t is None or t.numel() * t.element_size() != self.E * n or not t.is_contiguous()):
                 raise ValueError(f"{name} must be contiguous and hold {self.E} x {n} bytes")
-        if self.tensor_scale.dtype != torch.float32 or self.tensor_scale.numel() != 4 * self.E:
-            raise ValueError(f"tensor_scale must be float32 [{self.E}, 4]")
+        t = self.tensor_scale
+        if t.dtype != torch.float32 or t.numel() != 4 * self.E or not t.is_contiguous():
+            raise ValueError(f"tensor_scale must be contiguous float32 [{self.E}, 4]")
+        _one_device(self)
         return sharq_expert_weights(_ptr(self.codes), _ptr(self.scales_dense),
                                     _ptr(self.scales_sparse), _ptr(self.tensor_scale),
                                     self.K, self.N, self.E, self.cfg.c())

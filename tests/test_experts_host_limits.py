@@ -115,3 +115,41 @@ def test_plan_refuses(sq):  # noqa: F811
     for M, E, K in ((0, 0, 256), (1, -1, 256), (1, 0, 128), (1, 0, 300), (1, 0, 0)):
         assert f(M, E, K, r(a), r(b)) == 1
     assert f(1, 0, 256, None, r(b)) == 1 and f(1, 0, 256, r(a), None) == 1
+
+
+# ------------------------------------------------------------------ buffers of a weight
+
+def stacked(**other):
+    import torch
+
+    import fp4_sparse_dense_b200 as sq
+    E, K, N = 3, 256, 128
+    u8 = lambda n: torch.zeros(n, dtype=torch.uint8)  # noqa: E731
+    f = dict(codes=u8(E * N * K // 2), scales_dense=u8(E * N * K // 16), scales_sparse=u8(E * N * K // 32),
+             tensor_scale=torch.zeros(E, 4))
+    f.update(other)
+    return sq.ExpertWeights(*f.values(), K, N, E, sq.Config())
+
+
+def test_stacked_scales_have_to_be_contiguous(sq):  # noqa: F811
+    """A column range of a wider matrix holds as many numbers, elsewhere."""
+    import torch
+    assert stacked().c().E == 3
+    with pytest.raises(ValueError):
+        stacked(tensor_scale=torch.zeros(3, 8)[:, :4]).c()
+    with pytest.raises(ValueError):
+        stacked(tensor_scale=torch.zeros(4, 3).t()).c()
+
+
+@pytest.mark.parametrize("name", ["scales_dense", "scales_sparse", "tensor_scale"])
+def test_buffers_of_a_weight_are_on_one_device(sq, name):  # noqa: F811
+    """A pointer of another device never reaches a kernel."""
+    w = stacked()
+    setattr(w, name, getattr(w, name).to("meta"))
+    with pytest.raises(ValueError):
+        w.c()
+    one = stacked().expert(1)
+    assert one.c().K == 256
+    setattr(one, name, getattr(one, name).to("meta"))
+    with pytest.raises(ValueError):
+        one.c()
