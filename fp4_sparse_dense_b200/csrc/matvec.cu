@@ -21,19 +21,24 @@
 // unit they belong to, so that there is one prologue and one sum per CTA and slot. The warp that
 // has a unit's first step keeps its sums in registers and adds those of the warps behind it.
 // Where the activations do not fit, a cluster of S CTAs splits K, works through the same units
-// and adds its sums through distributed shared memory; the fewest CTAs that fit, since more only
-// move the cost (14336 x 4096 bf16, 4 rows: 15.1 us with one, 15.2 with two, 14.4 with four,
-// 15.3 with eight; 4096 x 28672: 18.2, 20.3, 21.2, 23.7). More rows go to tile_kernel
-// (matvec_tile.cu).
+// and adds its sums through distributed shared memory. The fewest CTAs that fit: at least 1, 2, 4,
+// 8 take, bf16 x NVFP4 / 32, 4096 x 28672, 1 row 14.4, 15.0, 17.1, 19.0 us, 8 rows 17.3, 17.1, 19.1,
+// 20.9. The fewest is not always the best: 14336 x 4096, 4 rows (two CTAs needed) 12.7, 12.1, 12.3 us
+// with two, four, eight; 4096 x 4096, 16 rows (two needed) 10.0, 9.0, 9.2. More rows go to
+// tile_kernel (matvec_tile.cu).
 //
-// Measured (B200, weights cycling through more than L2 or nearly so; N x K/2 codes and scales
-// over time): 4096 x 28672 NVFP4 / 16, 1 row 14.5 us (4.6 TB/s); 14336 x 4096, 8 rows 13.6 us
-// (2.3 TB/s); 4096 x 4096, 1 row 5.3 us (1.7 TB/s). The loop runs near memory rate; what remains
-// is the start (launch, activations, the first weights: about 3 us) and the sums and stores
-// (about 1 us), which a short weight cannot hide. The code that runs once per launch comes cold
-// from L2, so it is kept short: branches that depend on a vote or a shuffled warp index, known
-// to be uniform, took gate_up from 17.5 to 14.9 us, the prologue's copies in a loop another 0.2
-// us.
+// Measured (B200, weights cycling through more than L2; codes and scales over time): 4096 x 28672
+// bf16 x NVFP4 / 16, 1 row 14.7 us (4.5 TB/s); 14336 x 4096 fp16 x MXFP4, 8 rows 12.3 us (2.5 TB/s);
+// 4096 x 4096 bf16 x NVFP4 / 32, 1 row 5.8 us (1.5 TB/s; 5.3 with the weight in L2). The loop is bound
+// by its instructions, not by memory: a second weight of 4096 x 28672 (58.7 MB more of codes) adds
+// 13.6 us, two thirds of the copy rate, and the stalls are fixed latencies, a busy math pipe and
+// warps that were not selected before they are memory. What remains is the start (launch,
+// activations, the first weights: about 3 us) and the sums and stores (about 1 us), which a short
+// weight cannot hide. The code that runs once per launch comes cold from L2, so it is kept short:
+// branches that depend on a vote or a shuffled warp index, known to be uniform, took gate_up from
+// 17.5 to 14.9 us, the prologue's copies in a loop another 0.2 us. Sums in the owner's registers
+// helped where a slot has many rows (64 experts 30.4 -> 27.1 us, 14336 x 4096, 8 rows 13.2 -> 12.8)
+// and cost the shortest call (4096 x 4096, 1 row 4.9 -> 5.3).
 //
 // The widening sets the kernel's issue rate, so it uses the conversion instruction (two codes
 // to f16x2) and one packed multiply by the scale. That makes the weight an f16 operand:
@@ -836,11 +841,14 @@ cudaError_t launch_stream(MatvecParams p, int num_sms, unsigned long long ctx, c
 }
 
 // MMAs of eight rows that a slot takes, 0 where the tiles take the call. Measured, this kernel
-// against the tiles, us: one weight of 4096 x 28672, bf16, 8 rows 17 / 29, 9 rows 22 / 29, 16 rows
-// 26 / 29 (fp16 15 / 23, 19 / 23, 24 / 23); 14336 x 4096, 9 rows 15.2 / 17.5, 16 rows 16.4 / 17.7;
-// 4096 x 4096, 9 rows 9.5 / 8.9, 16 rows 9.7 / 9.2 (fp16 7.3 / 8.2, 7.9 / 8.4). Experts, whose
-// slots are seldom full, fp16: 8 of 14336 x 4096, 8 rows each on average 72 / 81, 12 rows 111 / 83
-// (two MMAs a slot; one: 103); 8 of 4096 x 28672, 8 rows 117 / 142, 12 rows 177 / 133.
+// against the tiles, us, NVFP4 / 32, bf16 (fp16): one weight of 4096 x 28672, 8 rows 17.3 / 29.1
+// (14.8 / 23.1), 9 rows 21.5 / 29.1 (19.2 / 23.1), 16 rows 25.8 / 29.3 (24.1 / 23.3); 14336 x 4096, 9
+// rows 15.8 / 17.6 (14.0 / 16.4), 16 rows 16.7 / 17.7 (14.9 / 16.3); 4096 x 4096, 8 rows 8.4 / 8.9
+// (6.4 / 8.2), 9 rows 10.1 / 8.9 (7.9 / 8.3), 16 rows 10.0 / 9.2 (8.1 / 8.5). One rule on rows, then:
+// it gives up a tenth on 9 to 16 bf16 rows of a small weight for more than that on the others.
+// Experts, whose slots are seldom full, fp16 x NVFP4 / 16, 8 experts, rows at random: 14336 x 4096, 8
+// rows each on average 72 / 78, 12 rows 106 / 83; 4096 x 28672, 8 rows 130 / 144, 12 rows 171 / 154
+// (two MMAs a slot: 96, 104 and 155, 179).
 int row_tiles(int M, int E, int K) {
   const int mt = (E > 0 ? M <= kRows * E : M <= kRows) ? 1 : E == 0 && M <= 2 * kRows ? 2 : 0;
   return mt > 0 && splits_for(K / kStepK, E > 0 ? kRows : M, E, mt) > 0 ? mt : 0;

@@ -624,8 +624,9 @@ cudaError_t launch_nc(const CUtensorMap& map, const MatvecParams& p, bool bf16, 
 
 }  // namespace
 
-// 16 or 32 (4096 x 6144, 16 rows: 11.8 us against 12.5; 21 rows: 18.5 against 12.7). An expert's
-// rows are not known here, twice their mean stands for them.
+// 16 or 32 (28672 x 4096, 16 bf16 rows, which is more than stream_kernel holds: 29.5 us against 30.9,
+// fp16 24.3 against 25.4; 4096 x 6144, 21 rows: 18.4 against 12.6; 4096 x 28672, 32 rows: 56.3
+// against 31.7). An expert's rows are not known here, twice their mean stands for them.
 int matvec_tile_rows(int M, int E) {
   const int want = E > 0 ? 2 * ((M + E - 1) / E) : M;
   return want <= 16 ? 16 : 32;
@@ -646,8 +647,8 @@ cudaError_t launch_matvec_tiles(const CUtensorMap& map, MatvecParams p, bool bf1
   }
   // K over a cluster of S CTAs, four steps each at least, where that gives the least time: S == 1
   // shares whole tiles out over the CTAs that run at once, S > 1 pays a CTA's start and end
-  // (about 6 steps) in every round. 4096 x 6144, 21 rows, S = 1, 2, 4, 8: 20.0, 13.2, 12.7, 16.4 us;
-  // 4096 x 28672, 16 rows: 29.2, 36.7, 42.7, 61.9.
+  // (about 6 steps) in every round. bf16, S = 1, 2, 4, 8: 4096 x 6144, 21 rows 19.8, 13.1, 12.6,
+  // 16.5 us; 4096 x 28672, 32 rows 31.9, 39.8, 47.1, 69.8; 28672 x 4096, 16 rows 111, 57.5, 31.5, 29.4.
   const int steps = p.K / kStepK;
   const double run = num_sms * 2.0, tiles = busy * (p.N / 128);
   auto rounds = [](double n) { return double((long long)(n + 0.999)); };

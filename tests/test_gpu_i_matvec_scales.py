@@ -161,3 +161,27 @@ def test_large_and_small_magnitudes(M, x_size, w_size):
     x64 = x.double().numpy()
     assert np.abs(x64 @ w64.T).max() < 2.0 ** 127 and np.abs(x64 @ w64.T).min() > 2.0 ** -126
     check(sq.matvec(x.cuda(), w, out_dtype=torch.float32), x64, w64, "f32")
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "bf16 beside a wide row"])
+@pytest.mark.parametrize("neighbours", ["apart", "alike"])
+def test_unit_rows_return_every_scale(kind, neighbours):
+    """x = e_k picks column k of the weight, exactly, at every E8M0 scale of a finite float32 weight,
+    subnormal values among them: with f16 operands, block by block, and with bf16 operands."""
+    import fp4_sparse_dense_b200 as sq
+    import torch
+    rng = np.random.default_rng(3)
+    K, N = 512, 128
+    if neighbours == "apart":
+        raw = (np.arange(N * K // 32) % 253).astype(np.uint8).reshape(N, K // 32)
+    else:  # a step's four blocks within two binades
+        raw = (np.arange(N * K // 128) % 250).repeat(4).reshape(N, K // 32) + rng.integers(0, 3, (N, K // 32))
+    w, w64 = with_scales(rng, raw.astype(np.uint8))
+    dt = torch.float16 if kind == "f16" else torch.bfloat16
+    eye = torch.eye(K, dtype=dt, device="cuda")
+    wide = torch.zeros(1, K, dtype=dt, device="cuda")
+    if kind.endswith("wide row"):
+        wide[0, 3], wide[0, 4] = 1e30, 1e-8
+    for k in range(0, K, 11):
+        y = sq.matvec(torch.cat((wide, eye[k:k + 11])), w, out_dtype=torch.float32)[1:]
+        assert np.array_equal(y.cpu().numpy().astype(np.float64), w64.T[k:k + 11]), k
