@@ -137,3 +137,71 @@ def test_experts_in_slots_of_sixteen_rows(counts, drop, fmt, mask, dtype):
 @pytest.mark.parametrize("fmt,dtype", [("nvfp4", "bf16"), ("mxfp4", "f16")])
 def test_experts_in_slots_of_thirty_two_rows(fmt, dtype):
     run_experts([40, 1, 0, 33], 2, 1024, 256, fmt, "pair48", dtype, (32, 0))
+
+
+def layer(sq, x, ids, probs, E, up, down, bufs):
+    """The steps of a layer of experts into buffers that are used again in every call."""
+    t, rows = sq.sort_tokens(ids, E, x, rows=bufs["rows"], out=bufs["tokens"])
+    h = sq.expert_matvec(rows, up, t, out=bufs["h"])
+    y = sq.expert_matvec(h, down, t, out=bufs["y"])
+    return sq.combine_tokens(y, t, probs, out=bufs["out"])
+
+
+@pytest.mark.parametrize("T,k,E,K,N", [(9, 2, 8, 14336, 256),     # products over clusters, one launch sorts
+                                       (700, 2, 200, 512, 256),   # a cluster sorts, the rows' kernel behind it
+                                       (600, 2, 5, 512, 256)])    # the tensor-memory kernel
+def test_chains_on_reused_buffers(T, k, E, K, N):
+    """One call after the other on the same buffers, without a wait between them, and the same
+    captured and replayed on two streams at once: the bits of calls that were waited for."""
+    import fp4_sparse_dense_b200 as sq
+    import torch
+    rng = np.random.default_rng(T)
+    cfg = cfg_of("nvfp4", "none")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    up, down = (sq.quantize_experts(torch.randn(E, *s, device="cuda", generator=g).mul_(0.02).to(torch.bfloat16), cfg)
+                for s in ((K, N), (N, K)))
+
+    def buffers():
+        bf = dict(dtype=torch.bfloat16, device="cuda")
+        i32 = dict(dtype=torch.int32, device="cuda")
+        tokens = sq.SortedTokens(torch.zeros(E + 1, **i32), torch.zeros(T * k, **i32), torch.zeros(T, k, **i32), T, k, E)
+        return dict(rows=torch.zeros(T * k, K, **bf), tokens=tokens, h=torch.zeros(T * k, N, **bf),
+                    y=torch.zeros(T * k, K, **bf), out=torch.zeros(T, K, **bf))
+
+    data = []
+    for i in range(4):
+        ids = rng.integers(-1 if i % 2 else 0, E, (T, k))
+        if i == 3:
+            ids[:] = -1  # nothing kept: the rows before stay in the buffers, the output is 0
+        data.append((to_device(heavy_activations(rng, T, K)), dev(ids), dev(rng.random((T, k)).astype(np.float32))))
+    bufs, want = buffers(), []
+    for d in data:
+        torch.cuda.synchronize()
+        want.append(layer(sq, *d, E, up, down, bufs).clone())
+        torch.cuda.synchronize()
+    assert (want[3] == 0).all() and not (want[0] == 0).all()
+
+    got = [layer(sq, *data[i], E, up, down, bufs).clone() for i in (0, 2, 3, 1, 0, 3, 2, 1) * 3]
+    for y, i in zip(got, (0, 2, 3, 1, 0, 3, 2, 1) * 3):
+        assert torch.equal(y, want[i])
+
+    graphs = []
+    for _ in range(2):
+        state, b = tuple(v.clone() for v in data[0]), buffers()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            layer(sq, *state, E, up, down, b)
+        graphs.append((graph, state, b["out"], torch.cuda.Stream()))
+    for pair in ((0, 1), (3, 2), (1, 3), (2, 0)):
+        torch.cuda.synchronize()
+        for (graph, state, _, s), i in zip(graphs, pair):
+            with torch.cuda.stream(s):
+                for dst, src in zip(state, data[i]):
+                    dst.copy_(src)
+                graph.replay()
+        torch.cuda.synchronize()
+        for (_, _, out, _), i in zip(graphs, pair):
+            assert torch.equal(out, want[i])
+    assert sq.sharq_device_status() == 0
